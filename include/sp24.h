@@ -7,7 +7,9 @@
  *   gemm     X, values, metadata (+ scales)  -> Y = X * W'^T
  * plus the INT8 calibration helpers (per-channel / per-tensor scales,
  * activation quantisation), the channel permutation search that may precede
- * pruning, and status queries.
+ * pruning, the same three verbs in e4m3 with block scales, an RMS norm that
+ * writes the 8-bit operand of either product (with its gradient), and status
+ * queries.
  *
  * Sources ("pages") are cited by title and section:
  *   [Ampere-sparsity] NVIDIA x Tencent MLPD article on Ampere fine-grained
@@ -65,10 +67,12 @@ typedef enum sp24_status {
 
 /* scoring modes for sp24_prune */
 enum { SP24_MAGNITUDE = 0, SP24_WANDA = 1 };
-/* value types of the compressed weight and of X in sp24_gemm */
-enum { SP24_BF16 = 0, SP24_INT8 = 1 };
-/* output kinds of sp24_gemm */
-enum { SP24_OUT_BF16 = 0, SP24_OUT_INT32 = 1, SP24_OUT_INT8 = 2 };
+/* value types: SP24_BF16 and SP24_INT8 of the compressed weight and of X in
+ * sp24_gemm, SP24_FP8 (e4m3) of sp24_gemm_fp8, and the element types of the
+ * norm's and quantisers' inputs (SP24_BF16, SP24_F32) */
+enum { SP24_BF16 = 0, SP24_INT8 = 1, SP24_FP8 = 2, SP24_F32 = 3 };
+/* output kinds of sp24_gemm, and SP24_OUT_BF16 / SP24_OUT_F32 of sp24_gemm_fp8 */
+enum { SP24_OUT_BF16 = 0, SP24_OUT_INT32 = 1, SP24_OUT_INT8 = 2, SP24_OUT_F32 = 3 };
 
 /* ------------------------------------------------------------------ sizes */
 
@@ -80,15 +84,22 @@ size_t sp24_mask_bytes(int64_t N, int64_t K);
 /* Bytes of the compressed values: N rows of K/2 kept values, in ascending
  * position order within each group ([Ampere-sparsity] Figure 1:
  * only the nonzeros are stored, 50 % of the value bytes).
- * dtype SP24_BF16 -> 2 bytes each, SP24_INT8 -> 1 byte each. */
+ * dtype SP24_BF16 -> 2 bytes each, SP24_INT8 and SP24_FP8 -> 1 byte each. */
 size_t sp24_vals_bytes(int64_t N, int64_t K, int dtype);
 
 /* Bytes of the metadata: 2 bits per kept value = 4 bits per group
  * ([Sparse-accel forum]; [Orin ch.7] 2.1 "Metadata (2-bit)"), stored in the
  * tcgen05.mma.sp operand layout: chunks of 128 rows x 128 K-positions
  * (2048 bytes), N rounded up to 128 and K rounded up to 128.
- * The layout depends on dtype but the size does not. */
+ * The layout depends on dtype but the size does not (SP24_FP8 has the layout
+ * of SP24_INT8). */
 size_t sp24_meta_bytes(int64_t N, int64_t K);
+
+/* Bytes of the e8m0 scales of e4m3 data: `rows` rows of 4 * ceil(K / 512)
+ * bytes, byte b of a row being the scale of its columns [128 b, 128 b + 128);
+ * bytes past the last block are padding, written as 127 (a scale of 1).
+ * rows = M for activations, ceil(N / 128) for a weight. */
+size_t sp24_scale_bytes(int64_t rows, int64_t K);
 
 /* Scratch bytes sp24_prune needs for `mode`: 8*K (float64 column norms) for
  * SP24_WANDA, 0 for SP24_MAGNITUDE. */
@@ -331,6 +342,8 @@ sp24_status sp24_gemm(const void* X, int64_t M, int64_t K, const void* vals,
  *   tile_tokens, tile_channels: output tile (rows of Y x columns of Y).
  *   split_k:       K slices per tile (1 unless "splitk").
  *   ctas, cluster: CTAs launched and CTAs per cluster.
+ * SP24_FP8 reports the launch of sp24_gemm_fp8, which has the kernels splitk
+ * (splits 1, 2, 4, 8), pair256, pair240 and pair224; other overrides are ignored.
  * Errors: SP24_ERR_ARG for a NULL plan, M < 1, N < 1, K < 16 or an unknown
  * dtype; SP24_ERR_CUDA if the device cannot be queried. */
 typedef struct sp24_gemm_plan_t {
@@ -343,6 +356,104 @@ typedef struct sp24_gemm_plan_t {
 } sp24_gemm_plan_t;
 
 sp24_status sp24_gemm_plan(int64_t M, int64_t N, int64_t K, int dtype, sp24_gemm_plan_t* plan);
+
+/* ------------------------------------------------ e4m3 with block scales */
+
+/* The 2:4 layer in e4m3 (8-bit floating point: 4 exponent and 3 mantissa bits,
+ * largest finite value 448, 0x7F = NaN) with a power-of-two scale for each
+ * block of 128 along K: per row for activations, per 128 rows for weights.
+ * (The pages quantise to int8 only, [Ampere-sparsity] "PTQ and QAT"; a scale
+ * per block needs no calibration run.)
+ * A scale is one e8m0 byte b standing for 2^(b - 127); it is the smallest
+ * power of two for which the block's largest magnitude is at most 448 times
+ * it (at least 2^-126; 1 for a block of zeros), so no value saturates and the
+ * only rounding is the code's own: round to nearest even, at most 2^-4 of a
+ * value whose scaled magnitude is at least 2^-6, else 2^-10 of the scale.
+ * A block that holds an infinity or a NaN becomes all NaN: scale byte 255 and
+ * codes 0x7F.  Scale rows are laid out as sp24_scale_bytes says. */
+
+/* e4m3 codes and scales of activations that no norm precedes:
+ *   X: bf16 or float32 [M][K] (x_dtype SP24_BF16 or SP24_F32).
+ *   Xq: e4m3 [M][K].  e_x: sp24_scale_bytes(M, K) bytes.
+ * Rules: M >= 0, K >= 1, K % 16 == 0 (K % 32 == 0 to multiply the result). */
+sp24_status sp24_quantize_fp8(const void* X, int64_t M, int64_t K, int x_dtype, void* Xq,
+                              uint8_t* e_x, void* stream);
+
+/* Weight conversion in one pass over W: the mask of sp24_prune (n_keep = 2;
+ * mode, norms, mask_in and mask_out as sp24_prune_compress), the kept values
+ * as e4m3 codes with one scale per 128 x 128 block of W (over the kept values
+ * only), and the metadata.
+ *   vals: e4m3 [N][K/2].  meta: sp24_meta_bytes(N, K) bytes.
+ *   e_w: sp24_scale_bytes(ceil(N / 128), K) bytes.
+ * Rules: N >= 0, K % 32 == 0; pointers 16-byte aligned. */
+sp24_status sp24_prune_compress_fp8(const void* W, int64_t N, int64_t K, int mode,
+                                    const double* norms, const uint8_t* mask_in,
+                                    uint8_t* mask_out, void* vals, void* meta, uint8_t* e_w,
+                                    void* stream);
+
+/* The same conversion under a given mask (sp24_compress in e4m3; a group that
+ * does not keep exactly two positions is reported as SP24_ERR_PATTERN). */
+sp24_status sp24_compress_fp8(const void* W, const uint8_t* mask, int64_t N, int64_t K, void* vals,
+                              void* meta, uint8_t* e_w, void* stream);
+
+/* Y = X * W'^T for e4m3 X and a 2:4 e4m3 weight:
+ *   Y[m][n] = sum over blocks b of 128 of 2^(e_x[m][b] - 127 + e_w[n / 128][b] - 127)
+ *             * sum over the kept k of block b of X[m][k] * W'[n][k],
+ * the tensor core applying the powers of two to the products; fp32 sums.
+ *   X, e_x: from sp24_quantize_fp8 or sp24_rmsnorm_quant.  vals, meta, e_w:
+ *   from sp24_prune_compress_fp8 or sp24_compress_fp8 with the same N and K.
+ *   out_kind SP24_OUT_BF16: Y bf16 [M][N] = rne(sum); SP24_OUT_F32: Y float32.
+ * Rules: M >= 0, N >= 0, N % 8 == 0, K >= 32, K % 32 == 0, pointers 16-byte
+ * aligned.  M = 1 (one token) runs the split-K kernel; sp24_gemm_plan with
+ * SP24_FP8 reports the launch. */
+sp24_status sp24_gemm_fp8(const void* X, const uint8_t* e_x, int64_t M, int64_t K,
+                          const void* vals, const void* meta, const uint8_t* e_w, int64_t N,
+                          int out_kind, void* Y, void* stream);
+
+/* --------------------------------------------- RMS norm, 8-bit output */
+
+/* Largest K of the norm (a row is held in one block's registers). */
+#define SP24_NORM_MAX_K 16384
+
+/* RMS norm of the residual stream with the operand of the next product as its
+ * output, in one pass:
+ *   h = X + R rounded to the stream's type (h = X without R);
+ *   s = 1 / sqrt(mean over the row of h^2 + eps), y = (h * s) * gamma, fp32;
+ *   out_dtype SP24_FP8:  Y e4m3 [M][K] with the scales e_y (as sp24_quantize_fp8
+ *                        of y: the operand of sp24_gemm_fp8);
+ *             SP24_INT8: Y int8 [M][K] = clamp(rint(y / *s_x), -127, 127), float32
+ *                        divide (as sp24_quantize of y: the operand of sp24_gemm
+ *                        with a calibrated per-tensor scale);
+ *             SP24_BF16: Y bf16 [M][K] = rne(y).
+ *   X, R (nullable), gamma [K], H (nullable): bf16 or float32 (x_dtype).  H
+ *   receives h and may be X or R (the stream updated in place).
+ *   rstd: float32 [M], receives s for sp24_rmsnorm_backward (nullable).
+ * Rules: M >= 0, 1 <= K <= SP24_NORM_MAX_K, K % 16 == 0, eps >= 0; e_y required
+ * for SP24_FP8, s_x (one float32, device) for SP24_INT8; pointers 16-byte
+ * aligned (rstd and s_x: 4).  A row of zeros gives zeros when eps > 0. */
+sp24_status sp24_rmsnorm_quant(const void* X, const void* R, const void* gamma, int64_t M,
+                               int64_t K, int x_dtype, float eps, int out_dtype, const float* s_x,
+                               void* H, void* Y, uint8_t* e_y, float* rstd, void* stream);
+
+/* Scratch bytes of sp24_rmsnorm_backward (partial sums of dgamma). */
+size_t sp24_rmsnorm_backward_workspace_bytes(int64_t M, int64_t K);
+
+/* Gradient of the norm for fine-tuning, the 8-bit rounding passed straight
+ * through: with g = dY * gamma and xh = H * rstd,
+ *   dX = rstd * (g - xh * mean over the row of (g * xh)) + dH,
+ *   dgamma = sum over the rows of dY * xh,
+ * fp32 sums in a fixed order (the same inputs give the same bits).
+ *   dY: gradient of y; dH (nullable): gradient that reaches h past the norm;
+ *   H: the h of the forward call; all bf16 or float32 [M][K] (x_dtype), as dX,
+ *   the gradient of X and of R.  dX may be dY or dH.  rstd: float32 [M].
+ *   dgamma: float32 [K] (zeros for M = 0).
+ *   workspace: sp24_rmsnorm_backward_workspace_bytes(M, K) bytes, in use until
+ *   the call's kernels have finished: calls that may overlap need one each.
+ * Rules: as sp24_rmsnorm_quant. */
+sp24_status sp24_rmsnorm_backward(const void* dY, const void* dH, const void* H, const void* gamma,
+                                  const float* rstd, int64_t M, int64_t K, int x_dtype, void* dX,
+                                  float* dgamma, void* workspace, size_t workspace_bytes,
+                                  void* stream);
 
 /* ------------------------------------------------------ 3x3 convolution */
 

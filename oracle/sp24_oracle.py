@@ -554,3 +554,87 @@ def im2col3x3(x: np.ndarray) -> np.ndarray:
             w0, w1 = max(0, -dw), min(ww, ww - dw)
             a[:, h0:h1, w0:w1, kh * 3 + kw, :] = x[:, h0 + dh:h1 + dh, w0 + dw:w1 + dw, :]
     return a.reshape(n * hh * ww, 9 * c)
+
+
+# ---------------------------------------------------------------------------
+# e4m3 with power-of-two block scales, and the RMS norm that writes it
+# (no page counterpart: the pages quantise to int8 only)
+# ---------------------------------------------------------------------------
+FP8_MAX = 448.0
+
+
+def e4m3_round(v: np.ndarray) -> np.ndarray:
+    """|v| <= 448 to the nearest value with 1 + 3 mantissa bits and a least
+    exponent of -6 (steps of 2^-9 below it), ties to the even code."""
+    v = np.asarray(v, dtype=np.float64)
+    _, x = np.frexp(v)                       # |v| in [2^(x-1), 2^x)
+    step = np.ldexp(1.0, np.maximum(x - 1, -6) - 3)
+    return np.rint(v / step) * step
+
+
+def block_exponent(amax: np.ndarray) -> np.ndarray:
+    """Smallest e >= -126 with amax <= 448 * 2^e; 0 for a block of zeros."""
+    amax = np.asarray(amax, dtype=np.float64)
+    _, x = np.frexp(amax)
+    e = np.maximum(x - 10, -126)
+    for _ in range(2):
+        e = np.where(FP8_MAX * np.ldexp(1.0, e) < amax, e + 1, e)
+    return np.where(amax > 0, e, 0).astype(np.int64)
+
+
+def fp8_rows(y: np.ndarray) -> Tuple[np.ndarray, np.ndarray]:
+    """(codes as values [M, K], exponents [M, ceil(K / 128)]) of y by rows and
+    blocks of 128 columns."""
+    y = np.asarray(y, dtype=np.float64)
+    m, k = y.shape
+    kb = (k + 127) // 128
+    q = np.empty_like(y)
+    e = np.empty((m, kb), dtype=np.int64)
+    for b in range(kb):
+        part = y[:, 128 * b:128 * b + 128]
+        e[:, b] = block_exponent(np.abs(part).max(axis=1))
+        q[:, 128 * b:128 * b + 128] = e4m3_round(part * np.ldexp(1.0, -e[:, b])[:, None])
+    return q, e
+
+
+def fp8_weight(w: np.ndarray, keep: np.ndarray) -> Tuple[np.ndarray, np.ndarray]:
+    """(dense masked codes as values [N, K], exponents [ceil(N/128), ceil(K/128)])."""
+    w = np.where(keep, np.asarray(w, dtype=np.float64), 0.0)
+    n, k = w.shape
+    q = np.empty_like(w)
+    e = np.empty(((n + 127) // 128, (k + 127) // 128), dtype=np.int64)
+    for i in range(e.shape[0]):
+        for b in range(e.shape[1]):
+            at = np.s_[128 * i:128 * i + 128, 128 * b:128 * b + 128]
+            e[i, b] = block_exponent(np.abs(w[at]).max())
+            q[at] = e4m3_round(w[at] * np.ldexp(1.0, -int(e[i, b])))
+    return q, e
+
+
+def fp8_gemm(xq: np.ndarray, ex: np.ndarray, wq: np.ndarray,
+             ew: np.ndarray) -> Tuple[np.ndarray, np.ndarray]:
+    """(Y, sum |x w|) of e4m3 codes with exponents: xq [M, K], ex [M, KB], dense
+    masked wq [N, K], ew [NB, KB]."""
+    m, k = xq.shape
+    n = wq.shape[0]
+    x = xq * np.ldexp(1.0, np.repeat(ex, 128, axis=1)[:, :k])
+    w = wq * np.ldexp(1.0, np.repeat(np.repeat(ew, 128, axis=0)[:n], 128, axis=1)[:, :k])
+    return x @ w.T, np.abs(x) @ np.abs(w).T
+
+
+def rmsnorm(h: np.ndarray, gamma: np.ndarray, eps: float) -> Tuple[np.ndarray, np.ndarray]:
+    """(y, 1 / rms) of the stored stream h [M, K]."""
+    h = np.asarray(h, dtype=np.float64)
+    s = 1.0 / np.sqrt((h * h).mean(axis=1) + eps)
+    return h * s[:, None] * np.asarray(gamma, dtype=np.float64), s
+
+
+def rmsnorm_backward(dy: np.ndarray, h: np.ndarray, gamma: np.ndarray, s: np.ndarray,
+                     dh: Optional[np.ndarray] = None) -> Tuple[np.ndarray, np.ndarray]:
+    """(dx, dgamma) of rmsnorm at h with s = 1 / rms."""
+    g = dy * gamma
+    xh = h * s[:, None]
+    dx = s[:, None] * (g - xh * (g * xh).mean(axis=1, keepdims=True))
+    if dh is not None:
+        dx = dx + dh
+    return dx, (dy * xh).sum(axis=0)

@@ -83,7 +83,7 @@ size_t sp24_mask_bytes(int64_t N, int64_t K) {
 
 size_t sp24_vals_bytes(int64_t N, int64_t K, int dtype) {
   if (N < 0 || K < 0 || (K % 8) != 0) return 0;
-  const size_t el = dtype == SP24_BF16 ? 2 : (dtype == SP24_INT8 ? 1 : 0);
+  const size_t el = dtype == SP24_BF16 ? 2 : ((dtype == SP24_INT8 || dtype == SP24_FP8) ? 1 : 0);
   return static_cast<size_t>(N) * static_cast<size_t>(K / 2) * el;
 }
 
@@ -92,6 +92,11 @@ size_t sp24_meta_bytes(int64_t N, int64_t K) {
   const size_t nr = static_cast<size_t>((N + 127) / 128);
   const size_t kc = static_cast<size_t>((K + 127) / 128);
   return nr * kc * 2048u;
+}
+
+size_t sp24_scale_bytes(int64_t rows, int64_t K) {
+  if (rows < 0 || K < 0) return 0;
+  return static_cast<size_t>(rows) * 4u * static_cast<size_t>((K + 511) / 512);
 }
 
 size_t sp24_prune_workspace_bytes(int64_t K, int mode) {

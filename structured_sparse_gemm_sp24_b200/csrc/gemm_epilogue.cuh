@@ -16,7 +16,7 @@
 // (N >= 32) it is done by stmatrix .trans on the mma fragment layout that the
 // 16x256b tensor-memory load produces: four instructions per warp and chunk,
 // into a box stored with the 64-byte swizzle so that the eight 16-byte rows
-// of each 8x8 matrix fall in distinct banks.  int32 and int8 outputs (and bf16
+// of each 8x8 matrix fall in distinct banks.  32-bit and int8 outputs (and bf16
 // with N < 32) take one store per token from the 32x32b load, where a thread
 // owns one channel and the warp writes whole box rows.
 #pragma once
@@ -35,9 +35,13 @@ constexpr int kEpiBox = 32;              // channels per warp store box
 constexpr int kConvProducerWarp = 2 + kEpiWarps;
 __host__ __device__ constexpr int gemm_threads(bool conv) { return 64 + kEpiThreads + (conv ? 64 : 0); }
 
+// The e4m3 product adds the same two warps: warp 10 lays out its block scales.
+constexpr int kScaleWarp = 2 + kEpiWarps;
+
 template <int OUTK>
 struct EpiOut {
-  static constexpr int kBytes = OUTK == SP24_OUT_INT32 ? 4 : (OUTK == SP24_OUT_INT8 ? 1 : 2);
+  static constexpr int kBytes = (OUTK == SP24_OUT_INT32 || OUTK == SP24_OUT_F32) ? 4
+                                : (OUTK == SP24_OUT_INT8 ? 1 : 2);
   static constexpr int kWarpBytes = kEpiChunk * kEpiBox * kBytes;   // one staging box
   static constexpr int kStagingBytes = kEpiWarps * kWarpBytes;
 };
@@ -62,7 +66,7 @@ struct EpiWarp {
 
 template <int kDtype>
 __device__ __forceinline__ float epi_value(uint32_t acc, float cscale) {
-  if constexpr (kDtype == SP24_BF16) return __uint_as_float(acc);
+  if constexpr (kDtype != SP24_INT8) return __uint_as_float(acc);
   return __fmul_rn(__int2float_rn(static_cast<int32_t>(acc)), cscale);
 }
 
@@ -111,10 +115,10 @@ __device__ __forceinline__ void stage_scalar(const uint32_t (&r)[32], uint8_t* s
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     const int e = t * cbox + lane;
-    if constexpr (kDtype == SP24_BF16) {
-      reinterpret_cast<__nv_bfloat16*>(stg)[e] = __float2bfloat16_rn(__uint_as_float(r[t]));
-    } else if constexpr (OUTK == SP24_OUT_INT32) {
+    if constexpr (OUTK == SP24_OUT_INT32 || OUTK == SP24_OUT_F32) {
       reinterpret_cast<uint32_t*>(stg)[e] = r[t];
+    } else if constexpr (kDtype != SP24_INT8) {
+      reinterpret_cast<__nv_bfloat16*>(stg)[e] = __float2bfloat16_rn(__uint_as_float(r[t]));
     } else {
       const float f = epi_value<kDtype>(r[t], cscale);
       if constexpr (OUTK == SP24_OUT_BF16) {

@@ -19,7 +19,9 @@
 //    empty: the even CTA's barrier collects one arrival per epilogue warp of
 //    both CTAs.
 // Warps: 0 = TMA producer (both CTAs), 1 = MMA issuer (even CTA), 2..9 =
-// epilogue (both CTAs; warp 2 also owns the tensor-memory allocation).
+// epilogue (both CTAs; warp 2 also owns the tensor-memory allocation), 10 (e4m3
+// only) = block scales (both CTAs: each needs the scales of all BN tokens and
+// of its own weight rows in its tensor memory).
 #pragma once
 
 namespace sp24 {
@@ -38,7 +40,10 @@ struct PairCfg {
   static constexpr int kMetaCols = 4 * kMetaChunks;
   static constexpr int kAcc = ACC;
   static constexpr int kMetaCol0 = kAcc * BN;
-  static constexpr int kTmemNeeded = kAcc * BN + 2 * kMetaCols;
+  // e4m3: as many scale buffers (two at most) as tensor memory has room for
+  static constexpr int kSfCol0 = kAcc * BN + 2 * kMetaCols;
+  using Sf = SfCfg<kDtype, BN, (512 - kSfCol0 >= 2 * SfCfg<kDtype, BN, 1>::kBufCols ? 2 : 1)>;
+  static constexpr int kTmemNeeded = kSfCol0 + Sf::kCols;
   static constexpr int kTmemCols = kTmemNeeded <= 32 ? 32
                                    : kTmemNeeded <= 64 ? 64
                                    : kTmemNeeded <= 128 ? 128
@@ -46,7 +51,10 @@ struct PairCfg {
   static constexpr int kOutBytes = EpiOut<OUTK>::kBytes;
   static constexpr int kStagingBytes = EpiOut<OUTK>::kStagingBytes;  // all epilogue warps
   static constexpr int kRingBytes = STAGES * kStageStride;
-  static constexpr int kSmemBytes = kRingBytes + kStagingBytes + 1024 + 256;
+  // scale buffers in shared memory: as many as stages, so a buffer's next load
+  // event comes at least STAGES iterations after the copy that reads it
+  static constexpr int kSfBytes = STAGES * Sf::kSmemBuf;
+  static constexpr int kSmemBytes = kRingBytes + kStagingBytes + kSfBytes + 1024 + 256;
   static_assert(kTmemNeeded <= 512, "tensor memory overflow");
   static_assert(BN % 16 == 0 && BN >= 64 && BN <= 256, "BN");
   static_assert(kSmemBytes <= 232448, "shared memory");
@@ -61,7 +69,7 @@ __device__ __forceinline__ uint32_t make_idesc_pair(uint32_t id2) {
 }
 
 template <int kDtype, int BN, int STAGES, int OUTK, int ACC, bool kConv = false>
-__global__ void __launch_bounds__(gemm_threads(kConv), 1)
+__global__ void __launch_bounds__(gemm_threads(kConv || kDtype == SP24_FP8), 1)
 gemm_sp_pair(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
              const __grid_constant__ CUtensorMap tmap_e, const __grid_constant__ CUtensorMap tmap_y,
              const __grid_constant__ CUtensorMap tmap_y16, const PersistArgs args) {
@@ -71,7 +79,8 @@ gemm_sp_pair(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   uint8_t* staging = smem + C::kRingBytes;
-  uint64_t* full_bar = reinterpret_cast<uint64_t*>(staging + C::kStagingBytes);
+  uint8_t* sf_smem = staging + C::kStagingBytes;
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(sf_smem + C::kSfBytes);
   uint64_t* empty_bar = full_bar + STAGES;
   uint64_t* tfull_bar = empty_bar + STAGES;
   uint64_t* tempty_bar = tfull_bar + C::kAcc;
@@ -88,7 +97,7 @@ gemm_sp_pair(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&full_bar[s], 1);
+      mbar_init(&full_bar[s], C::Sf::kOn ? 3 : 1);   // producer (and both scale loaders)
       mbar_init(&empty_bar[s], 1);
     }
     for (int a = 0; a < C::kAcc; ++a) {
@@ -165,6 +174,7 @@ gemm_sp_pair(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
     if (lane == 0 && rank == 0) {
       // ------------------------------------------------------ MMA issuer
       uint32_t it = 0, j = 0;
+      uint32_t sf_n = 0, sf_col = 0;   // scale loads so far, their current columns
       for (int tile = pair; tile < ntiles && !*abort_flag; tile += npairs, ++j) {
         const uint32_t acc = j % C::kAcc;
         if (!mbar_wait(&tempty_bar[acc], ((j / C::kAcc) & 1u) ^ 1u)) { *abort_flag = 1; break; }
@@ -175,6 +185,7 @@ gemm_sp_pair(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
           const int s = it % STAGES;
           const uint32_t ph = (it / STAGES) & 1u;
           if (!mbar_wait(&full_bar[s], ph)) { *abort_flag = 1; aborted = true; break; }
+          if constexpr (C::Sf::kOn) fence_acquire_cluster();   // the peer's scales
           tc_fence_after();
           uint8_t* st = smem + s * C::kStageStride;
           const uint32_t a_addr = smem_u32(st);
@@ -187,6 +198,14 @@ gemm_sp_pair(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
           for (int c = 0; c < C::kMetaChunks; ++c)
             tc_cp_128x128b_pair(tmem_base + meta_col + 4 * c,
                                 smem_desc(e_addr + 2048 * c, 128, 128, kSwizzleNone));
+          if constexpr (C::Sf::kOn) {
+            if (sf_load_stage(kb, 0)) {
+              sf_col = tmem_base + C::kSfCol0 + (sf_n % C::Sf::kBufs) * C::Sf::kBufCols;
+              sf_copy<typename C::Sf, true>(sf_col,
+                                            smem_u32(sf_smem) + (sf_n % STAGES) * C::Sf::kSmemBuf);
+              ++sf_n;
+            }
+          }
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             if (q < n_mma) {
@@ -197,6 +216,11 @@ gemm_sp_pair(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
               if constexpr (kDtype == SP24_BF16) {
                 tc_mma_sp_pair(d_tmem, a_desc, b_desc, tmem_base + meta_col + (q & ~1),
                                make_idesc_pair<kDtype, BN>(q & 1), accumulate);
+              } else if constexpr (kDtype == SP24_FP8) {
+                // byte of the scale word: this MMA's 128-position block mod 4
+                tc_mma_sp_fp8_pair(d_tmem, a_desc, b_desc, tmem_base + meta_col + 2 * q,
+                                   make_idesc_fp8<BN>(256, (kb & 1) * 2 + (q >> 1)),
+                                   sf_col + 4 * C::Sf::kTiles, sf_col, accumulate);
               } else {
                 tc_mma_sp_i8_pair(d_tmem, a_desc, b_desc, tmem_base + meta_col + 2 * q,
                                   make_idesc_pair<kDtype, BN>(0), accumulate);
@@ -243,6 +267,36 @@ gemm_sp_pair(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
       });
     }
     if (lane == 0) bulk_wait<0>();
+  } else if (C::Sf::kOn && warp == kScaleWarp) {
+    // ----------------------------------------------------- scale loader
+    if constexpr (C::Sf::kOn) {
+      uint32_t it = 0, sf_n = 0;
+      SfWords<BN> words;
+      const int64_t row_tiles128 = (args.n + 127) / 128;
+      for (int tile = pair; tile < ntiles && !*abort_flag; tile += npairs) {
+        int prt, tt;
+        tile_coords(tile, args, prt, tt);
+        const int64_t rt128 = prt * 2 + static_cast<int>(rank);
+        const int64_t tok0 = static_cast<int64_t>(tt) * BN;
+        words.load(args.e_x, args.e_w, args.sf_words, 0, tok0, args.m, rt128, row_tiles128, lane);
+        bool ok = true;
+        for (int kb = 0; kb < args.kblocks; ++kb, ++it) {
+          const int s = it % STAGES;
+          if (lane == 0) ok = mbar_wait(&empty_bar[s], ((it / STAGES) & 1u) ^ 1u);
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok) { *abort_flag = 1; break; }
+          if (sf_load_stage(kb, 0)) {
+            words.store(sf_smem + (sf_n % STAGES) * C::Sf::kSmemBuf, lane);
+            ++sf_n;
+            if (kb + 2 < args.kblocks)
+              words.load(args.e_x, args.e_w, args.sf_words, kb / 2 + 1, tok0, args.m, rt128,
+                         row_tiles128, lane);
+          }
+          if (lane == 0) mbar_arrive_release_cluster(map_peer(smem_u32(&full_bar[s]), 0));
+        }
+        if (!ok) break;
+      }
+    }
   }
 
   __syncwarp();
@@ -284,6 +338,7 @@ sp24_status launch_pair(const CUtensorMap& ma, const GemmArgs& g, const void* x,
                     static_cast<uint64_t>(rt128 * kchunks * 8), 32,
                     static_cast<uint32_t>(8 * C::kMetaChunks), CU_TENSOR_MAP_SWIZZLE_NONE));
   const CUtensorMapDataType ydt = OUTK == SP24_OUT_INT32 ? CU_TENSOR_MAP_DATA_TYPE_INT32
+                                  : OUTK == SP24_OUT_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                   : OUTK == SP24_OUT_INT8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                                           : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const int y_box = epi_box(g.n);
@@ -304,6 +359,9 @@ sp24_status launch_pair(const CUtensorMap& ma, const GemmArgs& g, const void* x,
   a.s_x = g.s_x;
   a.s_w = g.s_w;
   a.s_y = g.s_y;
+  a.e_x = g.e_x;
+  a.e_w = g.e_w;
+  a.sf_words = g.sf_words;
   a.m = g.m;
   a.n = g.n;
   a.k = g.k;
@@ -331,7 +389,8 @@ sp24_status launch_pair(const CUtensorMap& ma, const GemmArgs& g, const void* x,
   const int64_t ntiles = static_cast<int64_t>(a.row_tiles) * a.tok_tiles;
   if (ntiles > 0x7FFFFFFF) return SP24_ERR_UNSUPPORTED;
   if (pairs < 1 || pairs > ntiles) return SP24_ERR_ARG;   // the plan sizes the grid
-  return launch_kernel(kern, dim3(2 * pairs), dim3(gemm_threads(kConv)), C::kSmemBytes, s, 2, ma,
+  return launch_kernel(kern, dim3(2 * pairs), dim3(gemm_threads(kConv || C::Sf::kOn)),
+                       C::kSmemBytes, s, 2, ma,
                        mb, me, my, my16, a);
 }
 
@@ -374,12 +433,16 @@ inline sp24_status pair_capacity(int* out) {
   return SP24_OK;
 }
 
-// CTA-pair kernel for every output kind; ST = ring stages (ST32 with int32
+// CTA-pair kernel for every output kind; ST = ring stages (ST32 with 32-bit
 // output, whose staging is twice the size).
 template <int kDtype, int BN, int ST, int ST32, int ACC>
 sp24_status launch_pair_out(const CUtensorMap& ma, const GemmArgs& a, const void* x, int pairs,
                             cudaStream_t s) {
   if constexpr (kDtype == SP24_BF16) {
+    return launch_pair<kDtype, BN, ST, SP24_OUT_BF16, ACC>(ma, a, x, pairs, s);
+  } else if constexpr (kDtype == SP24_FP8) {
+    if (a.out_kind == SP24_OUT_F32)
+      return launch_pair<kDtype, BN, ST32, SP24_OUT_F32, ACC>(ma, a, x, pairs, s);
     return launch_pair<kDtype, BN, ST, SP24_OUT_BF16, ACC>(ma, a, x, pairs, s);
   } else {
     if (a.out_kind == SP24_OUT_INT32)

@@ -48,6 +48,9 @@ struct PersistArgs {
   const float* s_x;
   const float* s_w;
   const float* s_y;
+  const uint32_t* e_x;   // e4m3: scale words of the tokens [m][sf_words]
+  const uint32_t* e_w;   // and of the 128-row weight blocks
+  int64_t sf_words;      // scale words per row
   int64_t m, n, k;
   int kblocks;       // K stages per tile
   int row_tiles;     // ceil(N / 128)
@@ -373,6 +376,8 @@ sp24_status launch_persistent(const CUtensorMap& ma, const CUtensorMap& mb, cons
   a.s_x = g.s_x;
   a.s_w = g.s_w;
   a.s_y = g.s_y;
+  a.e_x = a.e_w = nullptr;
+  a.sf_words = 0;
   a.m = g.m;
   a.n = g.n;
   a.k = g.k;

@@ -1,5 +1,6 @@
 // libsp24: sparse GEMM Y = X * W'^T on the 5th-generation tensor cores
-// (tcgen05.mma.sp), for bf16 (fp32 accumulate) and int8 (int32 accumulate).
+// (tcgen05.mma.sp), for bf16 (fp32 accumulate), int8 (int32 accumulate) and
+// block-scaled e4m3 (fp32 accumulate).
 //
 // [Orin ch.7] "Chapter 7: 2:4 Structured Sparsity" 2.1 Step 3: the sparse
 // tensor core multiplies only the kept weights, each with the activation its
@@ -15,7 +16,8 @@
 //       tcgen05.cp into tensor memory, where tcgen05.mma.sp reads it;
 //   D = fp32 / int32 accumulator in tensor memory: lane = output channel,
 //       column = token.
-// Each stage issues 4 MMAs (K = 32 for kind::f16, 64 for kind::i8); both
+// Each stage issues 4 MMAs (K = 32 for kind::f16, 64 for kind::i8 and
+// kind::mxf8f6f4, which share the int8 tile and metadata layouts); all
 // advance A by 32 bytes and B by 64 bytes inside the swizzle atoms.
 //
 // Kernels: gemm_splitk.cuh (split-K), gemm_persistent.cuh (single-SM
@@ -43,6 +45,9 @@ struct GemmArgs {
   const float* s_x;
   const float* s_w;
   const float* s_y;
+  const uint32_t* e_x;   // e4m3: scale words (gemm_fp8.cuh)
+  const uint32_t* e_w;
+  int64_t sf_words;
   void* y;
   int64_t m, n, k;
   int kblocks;        // stages over the whole K
@@ -52,6 +57,7 @@ struct GemmArgs {
 
 }  // namespace sp24
 
+#include "gemm_fp8.cuh"
 #include "gemm_splitk.cuh"
 #include "gemm_epilogue.cuh"
 #include "gemm_persistent.cuh"
@@ -174,25 +180,30 @@ int small_ring_smem(int bn) {
 
 int small_ring_ctas_per_sm(int dtype, int bn) {
   const int smem = dtype == SP24_BF16 ? small_ring_smem<SP24_BF16>(bn)
-                                      : small_ring_smem<SP24_INT8>(bn);
+                   : dtype == SP24_FP8 ? small_ring_smem<SP24_FP8>(bn)
+                                       : small_ring_smem<SP24_INT8>(bn);
   return kSmemPerSm / (smem + 1024);
 }
 
 sp24_status make_plan(int64_t m, int64_t n, int kblocks, int dtype, Plan* p) {
   const int sms = sm_count();
   const int64_t row_tiles = (n + 127) / 128;
-  const int forced = impl_override();
+  int forced = impl_override();
+  // the e4m3 product has the split-K kernel and the 256, 240 and 224-token pairs
+  const bool fp8 = dtype == SP24_FP8;
+  if (fp8 && (forced == kSingle || forced == kPair192 || forced == kPair128)) forced = -1;
   // (an SP24_GEMM_IMPL override applies from half a wave of tiles, as the
   // kernel-family tests expect)
   const int64_t tiles128 = row_tiles * ((m + 127) / 128);
-  if (forced != kSplitK && m >= 128 && tiles128 >= (forced >= 0 ? sms / 2 : sms)) {
+  if (forced != kSplitK && m >= 128 && tiles128 >= (forced >= 0 ? sms / 2 : sms) &&
+      !(fp8 && forced < 0 && (m < 256 || (n < 256 && m <= 65535 * 128)))) {
     int pairs = 0;
     SP24_TRY(pair_capacity(&pairs));
     int impl = forced;
     if (impl < 0) {
       impl = kSingle;   // pair tiles need both dimensions to fill them
       if (m >= 256 && n >= 256) {
-        double best = est_time(kSingle, m, n, kblocks, sms, pairs);
+        double best = fp8 ? 1e30 : est_time(kSingle, m, n, kblocks, sms, pairs);
         for (int c : {kPair256, kPair240, kPair224}) {
           const double t = est_time(c, m, n, kblocks, sms, pairs);
           if (t < best) {
@@ -251,7 +262,7 @@ sp24_status make_plan(int64_t m, int64_t n, int kblocks, int dtype, Plan* p) {
     }
   }
   const int so = split_override();
-  if (so > 0 && so <= kblocks) split = so;
+  if (so > 0 && so <= kblocks) split = fp8 ? (so >= 8 ? 8 : so >= 4 ? 4 : so >= 2 ? 2 : 1) : so;
   p->impl = kSplitK;
   p->bn = bn;
   p->split = split;
@@ -266,15 +277,24 @@ sp24_status make_plan(int64_t m, int64_t n, int kblocks, int dtype, Plan* p) {
 template <int kDtype, int BN, int ST>
 sp24_status launch_split(int split, const CUtensorMap& ma, const CUtensorMap& mb,
                          const GemmArgs& a, cudaStream_t s) {
-  switch (split) {
-    case 1: return launch_gemm_cfg<kDtype, BN, ST, 1>(ma, mb, a, s);
-    case 2: return launch_gemm_cfg<kDtype, BN, ST, 2>(ma, mb, a, s);
-    case 3: return launch_gemm_cfg<kDtype, BN, ST, 3>(ma, mb, a, s);
-    case 4: return launch_gemm_cfg<kDtype, BN, ST, 4>(ma, mb, a, s);
-    case 5: return launch_gemm_cfg<kDtype, BN, ST, 5>(ma, mb, a, s);
-    case 6: return launch_gemm_cfg<kDtype, BN, ST, 6>(ma, mb, a, s);
-    case 7: return launch_gemm_cfg<kDtype, BN, ST, 7>(ma, mb, a, s);
-    default: return launch_gemm_cfg<kDtype, BN, ST, 8>(ma, mb, a, s);
+  if constexpr (kDtype == SP24_FP8) {   // powers of two only (the plan takes no other)
+    switch (split) {
+      case 1: return launch_gemm_cfg<kDtype, BN, ST, 1>(ma, mb, a, s);
+      case 2: return launch_gemm_cfg<kDtype, BN, ST, 2>(ma, mb, a, s);
+      case 4: return launch_gemm_cfg<kDtype, BN, ST, 4>(ma, mb, a, s);
+      default: return launch_gemm_cfg<kDtype, BN, ST, 8>(ma, mb, a, s);
+    }
+  } else {
+    switch (split) {
+      case 1: return launch_gemm_cfg<kDtype, BN, ST, 1>(ma, mb, a, s);
+      case 2: return launch_gemm_cfg<kDtype, BN, ST, 2>(ma, mb, a, s);
+      case 3: return launch_gemm_cfg<kDtype, BN, ST, 3>(ma, mb, a, s);
+      case 4: return launch_gemm_cfg<kDtype, BN, ST, 4>(ma, mb, a, s);
+      case 5: return launch_gemm_cfg<kDtype, BN, ST, 5>(ma, mb, a, s);
+      case 6: return launch_gemm_cfg<kDtype, BN, ST, 6>(ma, mb, a, s);
+      case 7: return launch_gemm_cfg<kDtype, BN, ST, 7>(ma, mb, a, s);
+      default: return launch_gemm_cfg<kDtype, BN, ST, 8>(ma, mb, a, s);
+    }
   }
 }
 
@@ -292,32 +312,46 @@ sp24_status dispatch(const void* x, const void* vals, GemmArgs a, cudaStream_t s
   SP24_TRY(make_map(&ma, vals, dt, el, static_cast<uint64_t>(a.k / 2),
                     static_cast<uint64_t>(a.n), box_cols, 128));
   const int pairs = static_cast<int>(p.ctas / 2);
-  switch (p.impl) {
-    case kPair256: return launch_pair_out<kDtype, 256, 4, 3, 1>(ma, a, x, pairs, s);
-    case kPair240: return launch_pair_out<kDtype, 240, 4, 3, 2>(ma, a, x, pairs, s);
-    case kPair224: return launch_pair_out<kDtype, 224, 4, 4, 2>(ma, a, x, pairs, s);
-    case kPair192: return launch_pair_out<kDtype, 192, 4, 4, 2>(ma, a, x, pairs, s);
-    case kPair128:
-      if constexpr (kDtype == SP24_BF16) {
-        return launch_pair<kDtype, 128, 6, SP24_OUT_BF16, 2>(ma, a, x, pairs, s);
-      } else {
-        if (a.out_kind == SP24_OUT_INT32)
-          return launch_pair<kDtype, 128, 5, SP24_OUT_INT32, 2>(ma, a, x, pairs, s);
-        if (a.out_kind == SP24_OUT_INT8)
-          return launch_pair<kDtype, 128, 6, SP24_OUT_INT8, 2>(ma, a, x, pairs, s);
-        return launch_pair<kDtype, 128, 5, SP24_OUT_BF16, 2>(ma, a, x, pairs, s);
-      }
-    default: break;
+  if constexpr (kDtype == SP24_FP8) {
+    // one stage fewer at 256 tokens (and 32-bit output): the scale buffers
+    switch (p.impl) {
+      case kPair256: return launch_pair_out<kDtype, 256, 3, 3, 1>(ma, a, x, pairs, s);
+      case kPair240: return launch_pair_out<kDtype, 240, 4, 3, 2>(ma, a, x, pairs, s);
+      case kPair224: return launch_pair_out<kDtype, 224, 4, 3, 2>(ma, a, x, pairs, s);
+      default: break;
+    }
+  } else {
+    switch (p.impl) {
+      case kPair256: return launch_pair_out<kDtype, 256, 4, 3, 1>(ma, a, x, pairs, s);
+      case kPair240: return launch_pair_out<kDtype, 240, 4, 3, 2>(ma, a, x, pairs, s);
+      case kPair224: return launch_pair_out<kDtype, 224, 4, 4, 2>(ma, a, x, pairs, s);
+      case kPair192: return launch_pair_out<kDtype, 192, 4, 4, 2>(ma, a, x, pairs, s);
+      case kPair128:
+        if constexpr (kDtype == SP24_BF16) {
+          return launch_pair<kDtype, 128, 6, SP24_OUT_BF16, 2>(ma, a, x, pairs, s);
+        } else {
+          if (a.out_kind == SP24_OUT_INT32)
+            return launch_pair<kDtype, 128, 5, SP24_OUT_INT32, 2>(ma, a, x, pairs, s);
+          if (a.out_kind == SP24_OUT_INT8)
+            return launch_pair<kDtype, 128, 6, SP24_OUT_INT8, 2>(ma, a, x, pairs, s);
+          return launch_pair<kDtype, 128, 5, SP24_OUT_BF16, 2>(ma, a, x, pairs, s);
+        }
+      default: break;
+    }
   }
   SP24_TRY(make_map(&mb, x, dt, el, static_cast<uint64_t>(a.k), static_cast<uint64_t>(a.m),
                     box_cols, static_cast<uint32_t>(bn)));
-  if (p.impl == kSingle) {
-    if constexpr (kDtype == SP24_BF16) {
-      return launch_persistent<kDtype, 128, 4, SP24_OUT_BF16>(ma, mb, a, s);
-    } else {
-      if (a.out_kind == SP24_OUT_INT32) return launch_persistent<kDtype, 128, 3, SP24_OUT_INT32>(ma, mb, a, s);
-      if (a.out_kind == SP24_OUT_INT8) return launch_persistent<kDtype, 128, 4, SP24_OUT_INT8>(ma, mb, a, s);
-      return launch_persistent<kDtype, 128, 4, SP24_OUT_BF16>(ma, mb, a, s);
+  if constexpr (kDtype != SP24_FP8) {
+    if (p.impl == kSingle) {
+      if constexpr (kDtype == SP24_BF16) {
+        return launch_persistent<kDtype, 128, 4, SP24_OUT_BF16>(ma, mb, a, s);
+      } else {
+        if (a.out_kind == SP24_OUT_INT32)
+          return launch_persistent<kDtype, 128, 3, SP24_OUT_INT32>(ma, mb, a, s);
+        if (a.out_kind == SP24_OUT_INT8)
+          return launch_persistent<kDtype, 128, 4, SP24_OUT_INT8>(ma, mb, a, s);
+        return launch_persistent<kDtype, 128, 4, SP24_OUT_BF16>(ma, mb, a, s);
+      }
     }
   }
   const int split = p.split;
@@ -329,7 +363,7 @@ sp24_status dispatch(const void* x, const void* vals, GemmArgs a, cudaStream_t s
     return launch_split<kDtype, BN_, ST_>(split, ma, mb, a, s);                             \
   }
   SP24_GEMM_CASE(16, 8)
-  SP24_GEMM_CASE(32, 8)
+  SP24_GEMM_CASE(32, (kDtype == SP24_FP8 ? 7 : 8))   // the scale buffers take one stage
   SP24_GEMM_CASE(64, 6)
   SP24_GEMM_CASE(128, 4)
 #undef SP24_GEMM_CASE
@@ -368,6 +402,8 @@ extern "C" sp24_status sp24_gemm(const void* X, int64_t M, int64_t K, const void
   a.s_x = s_x;
   a.s_w = s_w;
   a.s_y = s_y;
+  a.e_x = a.e_w = nullptr;
+  a.sf_words = 0;
   a.y = Y;
   a.m = M;
   a.n = N;
@@ -380,9 +416,42 @@ extern "C" sp24_status sp24_gemm(const void* X, int64_t M, int64_t K, const void
   return dispatch<SP24_INT8>(X, vals, a, as_stream(stream));
 }
 
+extern "C" sp24_status sp24_gemm_fp8(const void* X, const uint8_t* e_x, int64_t M, int64_t K,
+                                     const void* vals, const void* meta, const uint8_t* e_w,
+                                     int64_t N, int out_kind, void* Y, void* stream) {
+  if (M < 0 || N < 0 || K < 0 || (out_kind != SP24_OUT_BF16 && out_kind != SP24_OUT_F32))
+    return SP24_ERR_ARG;
+  if (M == 0 || N == 0) return SP24_OK;
+  if (!X || !e_x || !vals || !meta || !e_w || !Y) return SP24_ERR_ARG;
+  if (K < 32 || K % 32 != 0 || N % 8 != 0) return SP24_ERR_ALIGN;
+  if (!aligned16(X) || !aligned16(e_x) || !aligned16(vals) || !aligned16(meta) ||
+      !aligned16(e_w) || !aligned16(Y))
+    return SP24_ERR_ALIGN;
+  constexpr int64_t kMax = 0x7FFFFFFF - 512;   // tile coordinates are 32-bit
+  if (K > kMax || M > kMax || N > kMax)
+    return SP24_ERR_UNSUPPORTED;
+  SP24_TRY(check_device());
+  if (!get_encoder()) return cuda_fail("cudaGetDriverEntryPoint", "cuTensorMapEncodeTiled");
+  GemmArgs a;
+  a.meta = static_cast<const uint8_t*>(meta);
+  a.s_x = a.s_w = a.s_y = nullptr;
+  a.e_x = reinterpret_cast<const uint32_t*>(e_x);
+  a.e_w = reinterpret_cast<const uint32_t*>(e_w);
+  a.sf_words = (K + 511) / 512;
+  a.y = Y;
+  a.m = M;
+  a.n = N;
+  a.k = K;
+  a.out_kind = out_kind;
+  a.kblocks = static_cast<int>((K + 255) / 256);
+  a.kb_per_split = a.kblocks;
+  return dispatch<SP24_FP8>(X, vals, a, as_stream(stream));
+}
+
 extern "C" sp24_status sp24_gemm_plan(int64_t M, int64_t N, int64_t K, int dtype,
                                       sp24_gemm_plan_t* plan) {
-  if (!plan || M < 1 || N < 1 || K < 16 || (dtype != SP24_BF16 && dtype != SP24_INT8))
+  if (!plan || M < 1 || N < 1 || K < 16 ||
+      (dtype != SP24_BF16 && dtype != SP24_INT8 && dtype != SP24_FP8))
     return SP24_ERR_ARG;
   if (K > (int64_t(1) << 31) || M > (int64_t(1) << 31) || N > (int64_t(1) << 31))
     return SP24_ERR_UNSUPPORTED;

@@ -6,7 +6,8 @@
 // through distributed shared memory, so the result does not depend on timing.
 //
 // Warp roles (128 threads): warp 0 lane 0 issues TMA, warp 1 lane 0 issues
-// tcgen05 (copy + MMA), warp 2 owns the tensor-memory allocation; all four
+// tcgen05 (copy + MMA), warp 2 owns the tensor-memory allocation, warp 3 lays
+// out the block scales of an e4m3 product (gemm_fp8.cuh); all four
 // warps run the epilogue (tcgen05.ld of their 32 lanes -> scale / cast ->
 // shared-memory transpose -> coalesced 16-byte stores of Y rows).
 #pragma once
@@ -23,17 +24,28 @@ struct GemmCfg {
   static constexpr int kLogicalK = kDtype == SP24_BF16 ? 128 : 256;  // K per stage
   static constexpr int kMmaK = kLogicalK / 4;                        // K per MMA
   static constexpr int kMetaCols = 4 * kMetaChunks;                  // TMEM columns per stage
-  // accumulator columns [0, BN), two metadata buffers after it
+  // accumulator columns [0, BN), two metadata buffers after it, then (e4m3)
+  // two buffers of scales
+  using Sf = SfCfg<kDtype, BN, 2>;
   static constexpr int kMetaCol0 = BN;
-  static constexpr int kTmemNeeded = BN + 2 * kMetaCols;
+  static constexpr int kSfCol0 = BN + 2 * kMetaCols;
+  static constexpr int kTmemNeeded = BN + 2 * kMetaCols + Sf::kCols;
   static constexpr int kTmemCols = kTmemNeeded <= 32 ? 32
                                    : kTmemNeeded <= 64 ? 64
                                    : kTmemNeeded <= 128 ? 128
                                    : kTmemNeeded <= 256 ? 256 : 512;
   // stages are 1024-aligned: A, then the two B halves, then E
   static constexpr int kStageStride = (kStageBytes + 1023) / 1024 * 1024;
-  static constexpr int kSmemBytes = STAGES * kStageStride + 1024 /*align slack*/ + 256 /*bars*/;
+  // scale buffers in shared memory, after the ring.  A buffer is rewritten for
+  // the load event kSfBufs later and must have been copied by then: the loader
+  // waits for the stage of STAGES iterations ago, and two loads further on is
+  // at least three iterations later (a K range may start inside a word).
+  static constexpr int kSfBufs = STAGES <= 3 ? 2 : STAGES;
+  static constexpr int kSfBytes = kSfBufs * Sf::kSmemBuf;
+  static constexpr int kSmemBytes =
+      STAGES * kStageStride + kSfBytes + 1024 /*align slack*/ + 256 /*bars*/;
   static_assert(kTmemNeeded <= 512, "tensor memory overflow");
+  static_assert(kSmemBytes <= 232448, "shared memory");
   static_assert(BN % 16 == 0 && BN >= 16 && BN <= 256, "MMA N");
   // epilogue staging of a partial tile (fp32/int32, [BN][128]) reuses the ring
   static_assert(STAGES * kStageStride >= BN * 128 * 4, "staging does not fit");
@@ -49,7 +61,7 @@ gemm_sp_kernel(const __grid_constant__ CUtensorMap tmap_a,
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + STAGES * C::kStageStride);
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + STAGES * C::kStageStride + C::kSfBytes);
   uint64_t* empty_bar = full_bar + STAGES;
   uint64_t* accum_bar = empty_bar + STAGES;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(accum_bar + 1);
@@ -67,7 +79,7 @@ gemm_sp_kernel(const __grid_constant__ CUtensorMap tmap_a,
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&full_bar[s], 1);
+      mbar_init(&full_bar[s], C::Sf::kOn ? 2 : 1);   // producer (and scale loader)
       mbar_init(&empty_bar[s], 1);
     }
     mbar_init(accum_bar, 1);
@@ -96,7 +108,7 @@ gemm_sp_kernel(const __grid_constant__ CUtensorMap tmap_a,
       const int kb = kb_begin + i;
       uint8_t* st = smem + s * C::kStageStride;
       int chunks = C::kMetaChunks;
-      if (kDtype == SP24_INT8 && 2 * kb + 1 >= kchunks) chunks = 1;
+      if (C::kMetaChunks == 2 && 2 * kb + 1 >= kchunks) chunks = 1;
       mbar_arrive_expect_tx(&full_bar[s], C::kABytes + 2 * C::kBHalfBytes + 2048 * chunks);
       // A: compressed columns [kb*128B) of rows [row_tile*128, +128)
       tma_load_2d(st, &tmap_a, &full_bar[s], kb * (kDtype == SP24_BF16 ? 64 : 128),
@@ -116,6 +128,7 @@ gemm_sp_kernel(const __grid_constant__ CUtensorMap tmap_a,
   } else if (warp == 1 && lane == 0) {
     // ---------------------------------------------------------- MMA issuer
     const int64_t k_total = args.k;
+    uint32_t sf_n = 0, sf_col = 0;   // scale loads so far, their current columns
     for (int i = 0; i < n_iters; ++i) {
       const int s = i % STAGES;
       const uint32_t ph = (i / STAGES) & 1u;
@@ -138,6 +151,14 @@ gemm_sp_kernel(const __grid_constant__ CUtensorMap tmap_a,
         tc_cp_128x128b(tmem_base + meta_col + 4 * c,
                        smem_desc(e_addr + 2048 * c, 128, 128, kSwizzleNone));
       }
+      if constexpr (C::Sf::kOn) {
+        if (sf_load_stage(kb, kb_begin)) {
+          sf_col = tmem_base + C::kSfCol0 + (sf_n % C::Sf::kBufs) * C::Sf::kBufCols;
+          sf_copy<typename C::Sf, false>(
+              sf_col, smem_u32(smem + STAGES * C::kStageStride) + (sf_n % C::kSfBufs) * C::Sf::kSmemBuf);
+          ++sf_n;
+        }
+      }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if (j < n_mma) {
@@ -148,6 +169,11 @@ gemm_sp_kernel(const __grid_constant__ CUtensorMap tmap_a,
           if constexpr (kDtype == SP24_BF16) {
             tc_mma_sp(tmem_base, a_desc, b_desc, tmem_base + meta_col + (j & ~1),
                       make_idesc<kDtype, BN>(j & 1), accumulate);
+          } else if constexpr (kDtype == SP24_FP8) {
+            // byte of the scale word: this MMA's 128-position block mod 4
+            tc_mma_sp_fp8(tmem_base, a_desc, b_desc, tmem_base + meta_col + 2 * j,
+                          make_idesc_fp8<BN>(128, (kb & 1) * 2 + (j >> 1)),
+                          sf_col + 4 * C::Sf::kTiles, sf_col, accumulate);
           } else {
             tc_mma_sp_i8(tmem_base, a_desc, b_desc, tmem_base + meta_col + 2 * j,
                          make_idesc<kDtype, BN>(0), accumulate);
@@ -157,6 +183,32 @@ gemm_sp_kernel(const __grid_constant__ CUtensorMap tmap_a,
       tc_commit(&empty_bar[s]);   // frees the stage once these MMAs are done
     }
     tc_commit(accum_bar);         // accumulator complete
+  } else if (C::Sf::kOn && warp == 3) {
+    // -------------------------------------------------------- scale loader
+    if constexpr (C::Sf::kOn) {
+      uint32_t sf_n = 0;
+      SfWords<BN> words;
+      const int64_t tok0 = tok_tile * BN;
+      if (n_iters > 0)
+        words.load(args.e_x, args.e_w, args.sf_words, kb_begin / 2, tok0, args.m, row_tile,
+                   gridDim.y, lane);
+      for (int i = 0; i < n_iters; ++i) {
+        const int s = i % STAGES;
+        const int kb = kb_begin + i;
+        bool ok = true;
+        if (lane == 0) ok = mbar_wait(&empty_bar[s], ((i / STAGES) & 1u) ^ 1u);
+        if (!__shfl_sync(0xffffffffu, ok, 0)) { *abort_flag = 1; break; }
+        if (sf_load_stage(kb, kb_begin)) {
+          words.store(smem + STAGES * C::kStageStride + (sf_n % C::kSfBufs) * C::Sf::kSmemBuf, lane);
+          ++sf_n;
+          const int next = kb / 2 + 1;
+          if (2 * next < kb_end)
+            words.load(args.e_x, args.e_w, args.sf_words, next, tok0, args.m, row_tile, gridDim.y,
+                       lane);
+        }
+        if (lane == 0) mbar_arrive(&full_bar[s]);
+      }
+    }
   }
   __syncwarp();
 
@@ -209,7 +261,7 @@ gemm_sp_kernel(const __grid_constant__ CUtensorMap tmap_a,
       acc = ld_cluster_v4(map_peer(off, 0));
       for (int q = 1; q < SPLIT; ++q) {
         const uint4 p = ld_cluster_v4(map_peer(off, q));
-        if constexpr (kDtype == SP24_BF16) {
+        if constexpr (kDtype != SP24_INT8) {
           acc.x = __float_as_uint(__fadd_rn(__uint_as_float(acc.x), __uint_as_float(p.x)));
           acc.y = __float_as_uint(__fadd_rn(__uint_as_float(acc.y), __uint_as_float(p.y)));
           acc.z = __float_as_uint(__fadd_rn(__uint_as_float(acc.z), __uint_as_float(p.z)));
@@ -222,7 +274,10 @@ gemm_sp_kernel(const __grid_constant__ CUtensorMap tmap_a,
       acc = *reinterpret_cast<const uint4*>(stage32 + t * 128 + 4 * g);
     }
     const uint32_t a4[4] = {acc.x, acc.y, acc.z, acc.w};
-    if constexpr (kDtype == SP24_BF16) {
+    if (kDtype == SP24_FP8 && args.out_kind == SP24_OUT_F32) {
+      float* y = static_cast<float*>(args.y) + m_idx * args.n + n0;
+      *reinterpret_cast<uint4*>(y) = acc;
+    } else if constexpr (kDtype != SP24_INT8) {
       __nv_bfloat16* y = static_cast<__nv_bfloat16*>(args.y) + m_idx * args.n + n0;
       __nv_bfloat162 lo = __floats2bfloat162_rn(__uint_as_float(a4[0]), __uint_as_float(a4[1]));
       __nv_bfloat162 hi = __floats2bfloat162_rn(__uint_as_float(a4[2]), __uint_as_float(a4[3]));

@@ -5,3 +5,5 @@
 #include "gemm_sp.cu"
 #include "permute.cu"
 #include "conv.cu"
+#include "fp8.cu"
+#include "norm.cu"

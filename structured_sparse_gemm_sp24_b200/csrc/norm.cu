@@ -1,0 +1,633 @@
+// libsp24: RMS norm with the residual's addition and an 8-bit output
+// (sp24_rmsnorm_quant), its gradient (sp24_rmsnorm_backward), and the block
+// quantisation of an activation that no norm precedes (sp24_quantize_fp8).
+//
+//   h = round(x + r)                       the residual stream as stored
+//   s = 1 / sqrt(mean(h^2) + eps)          fp32 sums
+//   y = (h * s) * gamma                    fp32
+//   e4m3: one power-of-two scale per row and 128 columns (fp8.cuh)
+//   int8: clamp(rint(y / s_x), -127, 127), the rule of sp24_quantize
+//   bf16: y rounded
+//
+// Bound by HBM: each element of x and r is read once and h and y are written
+// once; a row lives in registers between its sum and its output.  A thread
+// holds NV vectors of 8 columns (16 bytes of bf16), T threads apart, so 16
+// neighbouring lanes hold a 128-column block and its maximum is four shuffles.
+// Rows of up to 1024 columns take one warp (no barrier); longer rows a block
+// of T threads and one barrier.  The grid is persistent, and a row's loads are
+// issued before the previous row is reduced and written.
+
+#include "fp8.cuh"
+#include "sp24_host.h"
+
+namespace sp24 {
+
+// ------------------------------------------------------- 8-element vectors
+// Loads that leave no line in L1 (each element is read once).
+__device__ __forceinline__ uint4 ld_stream16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+  return v;
+}
+
+template <typename T>
+struct Vec8;
+
+template <>
+struct Vec8<__nv_bfloat16> {
+  uint4 q;
+  __device__ __forceinline__ void zero() { q = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { q = ld_stream16(p); }
+  __device__ __forceinline__ void load_cached(const __nv_bfloat16* p) {
+    q = __ldg(reinterpret_cast<const uint4*>(p));
+  }
+  __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = q; }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+  __device__ __forceinline__ void set(const float (&f)[8]) {   // round to nearest even
+    q = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                   pack_bf16x2(f[6], f[7]));
+  }
+};
+
+template <>
+struct Vec8<float> {
+  uint4 a, b;
+  __device__ __forceinline__ void zero() { a = b = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void load(const float* p) {
+    a = ld_stream16(p);
+    b = ld_stream16(p + 4);
+  }
+  __device__ __forceinline__ void load_cached(const float* p) {
+    a = __ldg(reinterpret_cast<const uint4*>(p));
+    b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+  }
+  __device__ __forceinline__ void store(float* p) const {
+    reinterpret_cast<uint4*>(p)[0] = a;
+    reinterpret_cast<uint4*>(p)[1] = b;
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
+  }
+  __device__ __forceinline__ void set(const float (&f)[8]) {
+    a = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                   __float_as_uint(f[3]));
+    b = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]),
+                   __float_as_uint(f[7]));
+  }
+};
+
+// Sum over the threads of a row, the same value in all of them: the warp's by
+// shuffles, then (kWarpRow = false) the warps' in warp order through `part`,
+// which alternates between two rows' buffers so that one barrier is enough.
+template <bool kWarpRow>
+__device__ __forceinline__ float row_sum(float v, float (&part)[2][32], uint32_t buf) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  if constexpr (kWarpRow) return v;
+  const int warps = blockDim.x >> 5;
+  if ((threadIdx.x & 31) == 0) part[buf][threadIdx.x >> 5] = v;
+  __syncthreads();
+  float t = 0.0f;
+  for (int i = 0; i < warps; ++i) t += part[buf][i];
+  return t;
+}
+
+// ------------------------------------------------------------------ forward
+struct NormArgs {
+  const void* x;
+  const void* r;        // residual (optional)
+  const void* gamma;
+  void* h;              // x + r as stored (optional)
+  void* y;
+  uint8_t* e;           // e4m3: scale bytes [m][scale_cols]
+  float* rstd;          // optional
+  const float* s_x;     // int8: the given scale
+  int64_t m, k;
+  float eps;
+  int scale_cols;
+  int segs;             // column segments of a row (quantisation only, else 1)
+  int seg_len;          // columns per segment, a multiple of 512
+};
+
+template <typename T, int OUT, bool kNorm, int NV, bool kWarpRow>
+__global__ void __launch_bounds__(kWarpRow ? 256 : 1024)
+norm_kernel(const NormArgs a) {
+  pdl_launch_dependents();
+  pdl_wait_prior();
+  __shared__ float part[2][32];
+  const int lane = threadIdx.x & 31;
+  const int t = kWarpRow ? lane : static_cast<int>(threadIdx.x);
+  const int nt = kWarpRow ? 32 : static_cast<int>(blockDim.x);
+  const int64_t rows = a.m * a.segs;
+  const int per_cta = kWarpRow ? static_cast<int>(blockDim.x >> 5) : 1;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * per_cta + (kWarpRow ? threadIdx.x >> 5 : 0);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * per_cta;
+  const bool res = kNorm && a.r != nullptr;
+  const T* gamma = static_cast<const T*>(a.gamma);
+  float sx = 1.0f, rsx = 1.0f;
+  if constexpr (OUT == SP24_INT8) {
+    sx = *a.s_x;
+    rsx = __frcp_rn(sx);
+  }
+
+  Vec8<T> x[NV], r[NV];
+  auto load = [&](int64_t vr) {
+    const int64_t row = kNorm ? vr : vr / a.segs;
+    const int col0 = kNorm ? 0 : static_cast<int>(vr - row * a.segs) * a.seg_len;
+    const int64_t left = a.k - col0;
+    const int c_end = static_cast<int>((kNorm || left < a.seg_len ? left : a.seg_len) / 8);
+    const T* xp = static_cast<const T*>(a.x) + row * a.k + col0;
+    const T* rp = static_cast<const T*>(a.r) + row * a.k + col0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = t + i * nt;
+      if (c < c_end) {
+        x[i].load(xp + 8 * c);
+        if (res) r[i].load(rp + 8 * c);
+      } else {
+        x[i].zero();
+        if (res) r[i].zero();
+      }
+    }
+  };
+  if (first < rows) load(first);
+  uint32_t buf = 0;
+  for (int64_t vr = first; vr < rows; vr += step, buf ^= 1u) {
+    const int64_t row = kNorm ? vr : vr / a.segs;
+    const int seg = kNorm ? 0 : static_cast<int>(vr - row * a.segs);
+    const int col0 = seg * a.seg_len;
+    const int64_t left = a.k - col0;
+    const int c_end = static_cast<int>((kNorm || left < a.seg_len ? left : a.seg_len) / 8);
+    const int64_t base = row * a.k + col0;
+    Vec8<T> h[NV];
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = t + i * nt;
+      if (res) {
+        float fx[8], fr[8];
+        x[i].get(fx);
+        r[i].get(fr);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) fx[j] += fr[j];
+        h[i].set(fx);
+      } else {
+        h[i] = x[i];
+      }
+      if constexpr (kNorm) {
+        float f[8];
+        h[i].get(f);   // the norm is that of the stored sum
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum = __fmaf_rn(f[j], f[j], sum);
+        if (a.h != nullptr && c < c_end) h[i].store(static_cast<T*>(a.h) + base + 8 * c);
+      }
+    }
+    if (vr + step < rows) load(vr + step);
+    float rs = 1.0f;
+    if constexpr (kNorm) {
+      sum = row_sum<kWarpRow>(sum, part, buf);
+      rs = __frsqrt_rn(__fadd_rn(__fdiv_rn(sum, static_cast<float>(a.k)), a.eps));
+      if (a.rstd != nullptr && t == 0) a.rstd[row] = rs;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = t + i * nt;
+      const bool ok = c < c_end;
+      float f[8];
+      h[i].get(f);
+      if constexpr (kNorm) {
+        Vec8<T> g;
+        g.zero();
+        if (ok) g.load_cached(gamma + 8 * c);
+        float fg[8];
+        g.get(fg);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = __fmul_rn(__fmul_rn(f[j], rs), fg[j]);
+      }
+      if constexpr (OUT == SP24_FP8) {
+        uint32_t amax = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) amax = max(amax, abs_bits(f[j]));
+        if (!ok) amax = 0;   // (a NaN statistic makes NaNs of the zeros past the row)
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+        const uint32_t byte = scale_byte(amax);
+        const float inv = scale_inverse(byte == kScaleNan ? kScaleOne : byte);
+        if (ok) {
+          uint2 q;
+          q.x = e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
+          q.y = e4m3x4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv);
+          if (byte == kScaleNan) q.x = q.y = kCodeNan4;
+          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.y) + base + 8 * c) = q;
+          if ((lane & 15) == 0)
+            a.e[row * a.scale_cols + (col0 >> 7) + (c >> 4)] = static_cast<uint8_t>(byte);
+        }
+      } else if constexpr (OUT == SP24_INT8) {
+        if (ok) {
+          uint2 q;
+          q.x = q8(f[0], sx, rsx) | (q8(f[1], sx, rsx) << 8) | (q8(f[2], sx, rsx) << 16) |
+                (q8(f[3], sx, rsx) << 24);
+          q.y = q8(f[4], sx, rsx) | (q8(f[5], sx, rsx) << 8) | (q8(f[6], sx, rsx) << 16) |
+                (q8(f[7], sx, rsx) << 24);
+          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.y) + base + 8 * c) = q;
+        }
+      } else {
+        if (ok) {
+          Vec8<__nv_bfloat16> o;
+          o.set(f);
+          o.store(static_cast<__nv_bfloat16*>(a.y) + base + 8 * c);
+        }
+      }
+    }
+    if constexpr (OUT == SP24_FP8) {   // the scale row's padding
+      const int kb = static_cast<int>((a.k + 127) >> 7);
+      if (seg == a.segs - 1 && t < a.scale_cols - kb)
+        a.e[row * a.scale_cols + kb + t] = static_cast<uint8_t>(kScaleOne);
+    }
+  }
+}
+
+// ----------------------------------------------------------------- backward
+// With g = dy * gamma and xh = h * rstd:
+//   dx = rstd * (g - xh * mean(g * xh)) [+ dh],   dgamma = sum over rows dy * xh.
+// A thread keeps the dgamma sums of its columns over all rows of its block and
+// writes them once, to a row of the workspace; dgamma_kernel adds the rows in
+// order (no atomics: the same inputs give the same bits).
+struct BackArgs {
+  const void* dy;
+  const void* dh;       // optional
+  const void* h;
+  const void* gamma;
+  const float* rstd;
+  void* dx;
+  float* part;          // [gridDim.x][k]
+  int64_t m, k;
+};
+
+template <typename T, int NV, bool kWarpRow>
+__global__ void __launch_bounds__(kWarpRow ? 256 : (NV == 1 ? 1024 : 512))
+norm_back_kernel(const BackArgs a) {
+  pdl_launch_dependents();
+  pdl_wait_prior();
+  __shared__ float part[2][32];
+  extern __shared__ float s_acc[];   // kWarpRow: [8 warps][k]
+  const int lane = threadIdx.x & 31;
+  const int t = kWarpRow ? lane : static_cast<int>(threadIdx.x);
+  const int nt = kWarpRow ? 32 : static_cast<int>(blockDim.x);
+  const int per_cta = kWarpRow ? static_cast<int>(blockDim.x >> 5) : 1;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * per_cta + (kWarpRow ? threadIdx.x >> 5 : 0);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * per_cta;
+  const int c_end = static_cast<int>(a.k / 8);
+  const float inv_k = __fdiv_rn(1.0f, static_cast<float>(a.k));
+  const bool has_dh = a.dh != nullptr;
+
+  float acc[NV][8];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[i][j] = 0.0f;
+
+  Vec8<T> dy[NV], h[NV], dh[NV];
+  float rs_next = 0.0f;
+  auto load = [&](int64_t row) {
+    const int64_t base = row * a.k;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = t + i * nt;
+      if (c < c_end) {
+        dy[i].load(static_cast<const T*>(a.dy) + base + 8 * c);
+        h[i].load(static_cast<const T*>(a.h) + base + 8 * c);
+        if (has_dh) dh[i].load(static_cast<const T*>(a.dh) + base + 8 * c);
+      } else {
+        dy[i].zero();
+        h[i].zero();
+        if (has_dh) dh[i].zero();
+      }
+    }
+    rs_next = a.rstd[row];
+  };
+  if (first < a.m) load(first);
+  uint32_t buf = 0;
+  for (int64_t row = first; row < a.m; row += step, buf ^= 1u) {
+    const float rs = rs_next;
+    Vec8<T> cdy[NV], ch[NV], cdh[NV];
+    float dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = t + i * nt;
+      cdy[i] = dy[i];
+      ch[i] = h[i];
+      if (has_dh) cdh[i] = dh[i];
+      Vec8<T> g;
+      g.zero();
+      if (c < c_end) g.load_cached(static_cast<const T*>(a.gamma) + 8 * c);
+      float fd[8], fh[8], fg[8];
+      cdy[i].get(fd);
+      ch[i].get(fh);
+      g.get(fg);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float xh = fh[j] * rs;
+        acc[i][j] = __fmaf_rn(fd[j], xh, acc[i][j]);
+        dot = __fmaf_rn(fd[j] * fg[j], xh, dot);
+      }
+    }
+    if (row + step < a.m) load(row + step);
+    dot = row_sum<kWarpRow>(dot, part, buf);
+    const float mean = dot * inv_k;
+    T* out = static_cast<T*>(a.dx) + row * a.k;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = t + i * nt;
+      if (c < c_end) {
+        Vec8<T> g, o;
+        g.load_cached(static_cast<const T*>(a.gamma) + 8 * c);
+        float fd[8], fh[8], fg[8], fo[8];
+        cdy[i].get(fd);
+        ch[i].get(fh);
+        g.get(fg);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float xh = fh[j] * rs;
+          fo[j] = rs * (fd[j] * fg[j] - xh * mean);
+        }
+        if (has_dh) {
+          float f[8];
+          cdh[i].get(f);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) fo[j] += f[j];
+        }
+        o.set(fo);
+        o.store(out + 8 * c);
+      }
+    }
+  }
+  float* dst = a.part + static_cast<int64_t>(blockIdx.x) * a.k;
+  if constexpr (kWarpRow) {
+    // the warps' sums, added in warp order
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = t + i * nt;
+      if (c < c_end)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s_acc[(threadIdx.x >> 5) * a.k + 8 * c + j] = acc[i][j];
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < a.k; c += blockDim.x) {
+      float s = 0.0f;
+      for (int w = 0; w < per_cta; ++w) s += s_acc[w * a.k + c];
+      dst[c] = s;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = t + i * nt;
+      if (c < c_end) {
+        reinterpret_cast<float4*>(dst + 8 * c)[0] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+        reinterpret_cast<float4*>(dst + 8 * c)[1] = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
+      }
+    }
+  }
+}
+
+// dgamma[c] = sum over p rows of part, 32 columns per block: 32 groups of 8
+// threads (one float4 each) take every 32nd row, then the groups are added in
+// order.
+__global__ void __launch_bounds__(256) dgamma_kernel(const float* part, int p, int64_t k,
+                                                     float* dgamma) {
+  pdl_launch_dependents();
+  pdl_wait_prior();
+  __shared__ float s[32][33];
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + (threadIdx.x & 7) * 4;
+  const int grp = threadIdx.x >> 3;
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (c < k) {
+#pragma unroll 8
+    for (int i = grp; i < p; i += 32) {
+      const float4 q = __ldcg(reinterpret_cast<const float4*>(part + static_cast<int64_t>(i) * k + c));
+      v.x += q.x;
+      v.y += q.y;
+      v.z += q.z;
+      v.w += q.w;
+    }
+  }
+  float* d = &s[grp][(threadIdx.x & 7) * 4];
+  d[0] = v.x;
+  d[1] = v.y;
+  d[2] = v.z;
+  d[3] = v.w;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    float t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) t += s[i][threadIdx.x];
+    const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x;
+    if (col < k) dgamma[col] = t;
+  }
+}
+
+// -------------------------------------------------------------- launching
+// Resident blocks per SM of a kernel at `threads` threads, asked once per
+// device and block size.
+struct Occupancy {
+  std::atomic<int> per_sm[64][33];   // zero-initialised (static storage)
+};
+
+static sp24_status resident_blocks(const void* kern, Occupancy& o, int threads, size_t smem, int* out) {
+  int dev = 0;
+  if (const cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return cuda_fail("cudaGetDevice", e);
+  std::atomic<int>& slot = o.per_sm[dev & 63][threads / 32];
+  int n = slot.load(std::memory_order_acquire);
+  if (n == 0) {
+    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, smem);
+    if (e != cudaSuccess) return cuda_fail("cudaOccupancyMaxActiveBlocksPerMultiprocessor", e);
+    if (n < 1) return SP24_ERR_UNSUPPORTED;
+    slot.store(n, std::memory_order_release);
+  }
+  *out = n;
+  return SP24_OK;
+}
+
+template <typename T, int OUT, bool kNorm, int NV, bool kWarpRow>
+static sp24_status launch_norm_t(const NormArgs& a, int threads, cudaStream_t s) {
+  auto kern = norm_kernel<T, OUT, kNorm, NV, kWarpRow>;
+  static Occupancy occ;
+  int per_sm = 0;
+  SP24_TRY(resident_blocks(reinterpret_cast<const void*>(kern), occ, threads, 0, &per_sm));
+  const int64_t per_cta = kWarpRow ? threads / 32 : 1;
+  const int64_t ctas = (a.m * a.segs + per_cta - 1) / per_cta;
+  const int64_t cap = static_cast<int64_t>(sm_count()) * per_sm;
+  return launch_kernel(kern, dim3(static_cast<unsigned>(ctas < cap ? ctas : cap)), dim3(threads), 0,
+                       s, 1, a);
+}
+
+static int round32(int64_t v) { return static_cast<int>((v + 31) / 32 * 32); }
+
+template <typename T, int OUT, bool kNorm>
+static sp24_status launch_norm(const NormArgs& a, cudaStream_t s) {
+  const int64_t c = (kNorm || a.k < a.seg_len ? a.k : a.seg_len) / 8;   // vectors of a row
+  if (c <= 32) return launch_norm_t<T, OUT, kNorm, 1, true>(a, 256, s);
+  if (c <= 64) return launch_norm_t<T, OUT, kNorm, 2, true>(a, 256, s);
+  if (c <= 128) return launch_norm_t<T, OUT, kNorm, 4, true>(a, 256, s);
+  if (c <= 1024 && a.m * a.segs <= 2 * sm_count())
+    return launch_norm_t<T, OUT, kNorm, 1, false>(a, round32(c), s);
+  return launch_norm_t<T, OUT, kNorm, 2, false>(a, round32((c + 1) / 2), s);
+}
+
+template <bool kNorm>
+static sp24_status launch_norm_out(const NormArgs& a, int x_dtype, int out, cudaStream_t s) {
+  if constexpr (!kNorm) {
+    return x_dtype == SP24_F32 ? launch_norm<float, SP24_FP8, false>(a, s)
+                               : launch_norm<__nv_bfloat16, SP24_FP8, false>(a, s);
+  } else {
+    const bool f32 = x_dtype == SP24_F32;
+    switch (out) {
+      case SP24_FP8:
+        return f32 ? launch_norm<float, SP24_FP8, true>(a, s)
+                   : launch_norm<__nv_bfloat16, SP24_FP8, true>(a, s);
+      case SP24_INT8:
+        return f32 ? launch_norm<float, SP24_INT8, true>(a, s)
+                   : launch_norm<__nv_bfloat16, SP24_INT8, true>(a, s);
+      default:
+        return f32 ? launch_norm<float, SP24_BF16, true>(a, s)
+                   : launch_norm<__nv_bfloat16, SP24_BF16, true>(a, s);
+    }
+  }
+}
+
+// Rows of the dgamma workspace: at most this many blocks run the backward.
+constexpr int64_t kBackMaxCtas = 640;
+
+template <typename T, int NV, bool kWarpRow>
+static sp24_status launch_back_t(const BackArgs& a, int threads, float* dgamma, cudaStream_t s) {
+  auto kern = norm_back_kernel<T, NV, kWarpRow>;
+  static Occupancy occ;
+  const size_t smem = kWarpRow ? static_cast<size_t>(threads / 32) * a.k * 4 : 0;
+  int per_sm = 0;
+  SP24_TRY(resident_blocks(reinterpret_cast<const void*>(kern), occ, threads, smem, &per_sm));
+  const int64_t per_cta = kWarpRow ? threads / 32 : 1;
+  int64_t ctas = (a.m + per_cta - 1) / per_cta;
+  const int64_t cap = static_cast<int64_t>(sm_count()) * per_sm;
+  if (ctas > cap) ctas = cap;
+  if (ctas > kBackMaxCtas) ctas = kBackMaxCtas;
+  if (ctas > 0)
+    SP24_TRY(launch_kernel(kern, dim3(static_cast<unsigned>(ctas)), dim3(threads), smem, s, 1, a));
+  return launch_kernel(dgamma_kernel, dim3(static_cast<unsigned>((a.k + 31) / 32)), dim3(256), 0, s,
+                       1, static_cast<const float*>(a.part), static_cast<int>(ctas), a.k, dgamma);
+}
+
+template <typename T>
+static sp24_status launch_back(const BackArgs& a, float* dgamma, cudaStream_t s) {
+  const int64_t c = a.k / 8;
+  if (c <= 32) return launch_back_t<T, 1, true>(a, 256, dgamma, s);
+  if (c <= 64) return launch_back_t<T, 2, true>(a, 256, dgamma, s);
+  if (c <= 128) return launch_back_t<T, 4, true>(a, 256, dgamma, s);
+  if (c <= 1024) return launch_back_t<T, 2, false>(a, round32((c + 1) / 2), dgamma, s);
+  return launch_back_t<T, 4, false>(a, round32((c + 3) / 4), dgamma, s);
+}
+
+}  // namespace sp24
+
+using namespace sp24;
+
+extern "C" {
+
+sp24_status sp24_rmsnorm_quant(const void* X, const void* R, const void* gamma, int64_t M,
+                               int64_t K, int x_dtype, float eps, int out_dtype, const float* s_x,
+                               void* H, void* Y, uint8_t* e_y, float* rstd, void* stream) {
+  if (M < 0 || K < 1 || (x_dtype != SP24_BF16 && x_dtype != SP24_F32) ||
+      (out_dtype != SP24_FP8 && out_dtype != SP24_INT8 && out_dtype != SP24_BF16) || !(eps >= 0.0f))
+    return SP24_ERR_ARG;
+  if (K % 16 != 0) return SP24_ERR_ALIGN;
+  if (K > SP24_NORM_MAX_K) return SP24_ERR_UNSUPPORTED;
+  if (M == 0) return SP24_OK;
+  if (!X || !gamma || !Y || (out_dtype == SP24_FP8 && !e_y) || (out_dtype == SP24_INT8 && !s_x))
+    return SP24_ERR_ARG;
+  if (!aligned16(X) || !aligned16(gamma) || !aligned16(Y) || (R && !aligned16(R)) ||
+      (H && !aligned16(H)) || (out_dtype == SP24_FP8 && !aligned16(e_y)))
+    return SP24_ERR_ALIGN;
+  SP24_TRY(check_device());
+  NormArgs a{};
+  a.x = X;
+  a.r = R;
+  a.gamma = gamma;
+  a.h = H;
+  a.y = Y;
+  a.e = e_y;
+  a.rstd = rstd;
+  a.s_x = s_x;
+  a.m = M;
+  a.k = K;
+  a.eps = eps;
+  a.scale_cols = static_cast<int>(4 * ((K + 511) / 512));
+  a.segs = 1;
+  a.seg_len = 0;
+  return launch_norm_out<true>(a, x_dtype, out_dtype, as_stream(stream));
+}
+
+sp24_status sp24_quantize_fp8(const void* X, int64_t M, int64_t K, int x_dtype, void* Xq,
+                              uint8_t* e_x, void* stream) {
+  if (M < 0 || K < 1 || (x_dtype != SP24_BF16 && x_dtype != SP24_F32)) return SP24_ERR_ARG;
+  if (K % 16 != 0) return SP24_ERR_ALIGN;
+  if (M == 0) return SP24_OK;
+  if (!X || !Xq || !e_x) return SP24_ERR_ARG;
+  if (!aligned16(X) || !aligned16(Xq) || !aligned16(e_x)) return SP24_ERR_ALIGN;
+  if (K > 0x7FFFFFFF - 4096) return SP24_ERR_UNSUPPORTED;
+  SP24_TRY(check_device());
+  NormArgs a{};
+  a.x = X;
+  a.y = Xq;
+  a.e = e_x;
+  a.m = M;
+  a.k = K;
+  a.scale_cols = static_cast<int>(4 * ((K + 511) / 512));
+  a.seg_len = 4096;
+  a.segs = static_cast<int>((K + a.seg_len - 1) / a.seg_len);
+  return launch_norm_out<false>(a, x_dtype, SP24_FP8, as_stream(stream));
+}
+
+size_t sp24_rmsnorm_backward_workspace_bytes(int64_t M, int64_t K) {
+  if (M < 0 || K < 1 || K > SP24_NORM_MAX_K) return 0;
+  const int64_t rows = M < 1 ? 1 : (M < kBackMaxCtas ? M : kBackMaxCtas);
+  return static_cast<size_t>(rows) * static_cast<size_t>(K) * sizeof(float);
+}
+
+sp24_status sp24_rmsnorm_backward(const void* dY, const void* dH, const void* H, const void* gamma,
+                                  const float* rstd, int64_t M, int64_t K, int x_dtype, void* dX,
+                                  float* dgamma, void* workspace, size_t workspace_bytes,
+                                  void* stream) {
+  if (M < 0 || K < 1 || (x_dtype != SP24_BF16 && x_dtype != SP24_F32)) return SP24_ERR_ARG;
+  if (K % 16 != 0) return SP24_ERR_ALIGN;
+  if (K > SP24_NORM_MAX_K) return SP24_ERR_UNSUPPORTED;
+  if (!dgamma || !workspace || workspace_bytes < sp24_rmsnorm_backward_workspace_bytes(M, K))
+    return SP24_ERR_ARG;
+  if (M > 0 && (!dY || !H || !gamma || !rstd || !dX)) return SP24_ERR_ARG;
+  if (!aligned16(dgamma) || !aligned16(workspace) || (M > 0 && (!aligned16(dY) || !aligned16(H) ||
+      !aligned16(gamma) || !aligned16(dX))) || (dH && !aligned16(dH)))
+    return SP24_ERR_ALIGN;
+  SP24_TRY(check_device());
+  BackArgs a{};
+  a.dy = dY;
+  a.dh = dH;
+  a.h = H;
+  a.gamma = gamma;
+  a.rstd = rstd;
+  a.dx = dX;
+  a.part = static_cast<float*>(workspace);
+  a.m = M;
+  a.k = K;
+  return x_dtype == SP24_F32 ? launch_back<float>(a, dgamma, as_stream(stream))
+                             : launch_back<__nv_bfloat16>(a, dgamma, as_stream(stream));
+}
+
+}  // extern "C"

@@ -215,6 +215,60 @@ __device__ __forceinline__ uint32_t make_idesc(uint32_t id2) {
          (static_cast<uint32_t>(BN >> 3) << 17) | ((128u >> 4) << 24);
 }
 
+// --------------------------------------- block-scaled e4m3 (kind::mxf8f6f4)
+// D += (A * 2^ea) * (B * 2^eb)^T: the tensor core multiplies the K = 64
+// products of a row of A and a row of B by the power-of-two scales (e8m0
+// bytes) that tensor memory holds for the two rows.  Scale layout: the 32-bit
+// word of row r (of at most 128) sits in lane r % 32 (repeated in the four
+// lane quadrants), column r / 32; its four bytes are the scales of four
+// consecutive K blocks, and the instruction descriptor names the byte.
+__device__ __forceinline__ void tc_mma_sp_fp8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                              uint32_t e_tmem, uint32_t idesc, uint32_t sfa_tmem,
+                                              uint32_t sfb_tmem, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %7, 0;\n\t"
+      "tcgen05.mma.sp.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X"
+      " [%0], %1, %2, [%3], %4, [%5], [%6], p;\n\t}"
+      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(e_tmem), "r"(idesc), "r"(sfa_tmem),
+        "r"(sfb_tmem), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tc_mma_sp_fp8_pair(uint32_t d_tmem, uint64_t a_desc,
+                                                   uint64_t b_desc, uint32_t e_tmem,
+                                                   uint32_t idesc, uint32_t sfa_tmem,
+                                                   uint32_t sfb_tmem, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %7, 0;\n\t"
+      "tcgen05.mma.sp.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X"
+      " [%0], %1, %2, [%3], %4, [%5], [%6], p;\n\t}"
+      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(e_tmem), "r"(idesc), "r"(sfa_tmem),
+        "r"(sfb_tmem), "r"(accumulate)
+      : "memory");
+}
+
+// Copies a 32-lane x 16-byte tile of scales from shared memory into all four
+// lane quadrants, columns [taddr, taddr + 4).
+__device__ __forceinline__ void tc_cp_scales(uint32_t taddr, uint64_t sdesc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc)
+               : "memory");
+}
+__device__ __forceinline__ void tc_cp_scales_pair(uint32_t taddr, uint64_t sdesc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc)
+               : "memory");
+}
+
+// Instruction descriptor of the block-scaled sparse MMA: e4m3 A and B (format
+// 0), e8m0 scales, `rows` MMA rows (128, or 256 for a pair), `sf` the byte of
+// the scale words of both operands.
+template <int BN>
+__device__ __forceinline__ uint32_t make_idesc_fp8(uint32_t rows, uint32_t sf) {
+  return (1u << 2) | (sf << 4) | (static_cast<uint32_t>(BN >> 3) << 17) | (1u << 23) |
+         ((rows >> 4) << 24) | (sf << 29);
+}
+
 // Each thread of the warp reads 16 consecutive 32-bit columns of its own lane
 // (warp w of the CTA reaches lanes 32*(w%4) .. 32*(w%4)+31).
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
@@ -454,6 +508,19 @@ __device__ __forceinline__ void tc_commit_pair_mc(uint64_t* bar, uint16_t cta_ma
 // cluster-scope ordering of this thread's memory operations is needed.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
+
+// Arrival that also releases this thread's earlier writes (shared memory of
+// its own CTA included) to the threads of the cluster that wait on `bar`.
+__device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];"
+               ::"r"(bar_cluster) : "memory");
+}
+
+// Orders what the phase that just completed on an mbarrier released at cluster
+// scope before this thread's later accesses.
+__device__ __forceinline__ void fence_acquire_cluster() {
+  asm volatile("fence.acq_rel.cluster;" ::: "memory");
 }
 
 // ------------------------------------------------------------------ cluster

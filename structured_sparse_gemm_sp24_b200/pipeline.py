@@ -5,7 +5,7 @@ the library's kernels through :mod:`structured_sparse_gemm_sp24_b200.sp24`.
 """
 from __future__ import annotations
 
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 import torch
 
@@ -123,6 +123,111 @@ def gemm(X: torch.Tensor, vals: torch.Tensor, meta: torch.Tensor, N: int,
         out = torch.empty((M, N), dtype=odt, device=X.device)
     _b.sp24_gemm(X, vals, meta, N, dtype, s_x, s_w, out_kind, s_y, out)
     return out
+
+
+def _scales(rows: int, K: int, device) -> torch.Tensor:
+    return torch.empty((rows, 4 * ((K + 511) // 512)), dtype=torch.float8_e8m0fnu, device=device)
+
+
+def quantize_fp8(X: torch.Tensor, out: Optional[torch.Tensor] = None,
+                 out_scales: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """e4m3 codes [M, K] of X (bf16 or float32) and the e8m0 scales of each row's
+    blocks of 128 columns [M, 4 * ceil(K / 512)] (columns past the last block: 1)."""
+    M, K = X.shape
+    if out is None:
+        out = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=X.device)
+    if out_scales is None:
+        out_scales = _scales(M, K, X.device)
+    _b.sp24_quantize_fp8(X, out, out_scales)
+    return out, out_scales
+
+
+def _alloc_fp8_weight(N: int, K: int, device):
+    return (torch.empty((N, K // 2), dtype=torch.float8_e4m3fn, device=device),
+            torch.empty(_b.sp24_meta_bytes(N, K), dtype=torch.uint8, device=device),
+            _scales((N + 127) // 128, K, device))
+
+
+def prune_compress_fp8(W: torch.Tensor, mode: int = _b.SP24_MAGNITUDE,
+                       norms: Optional[torch.Tensor] = None,
+                       mask_in: Optional[torch.Tensor] = None, want_mask: bool = False):
+    """e4m3 weight conversion in one pass: (vals e4m3 [N, K/2], meta, e_w[, mask])
+    with one e8m0 scale per 128 x 128 block."""
+    N, K = W.shape
+    vals, meta, e_w = _alloc_fp8_weight(N, K, W.device)
+    mask = torch.empty((N, K // 8), dtype=torch.uint8, device=W.device) if want_mask else None
+    _b.sp24_prune_compress_fp8(W, mode, norms, mask_in, mask, vals, meta, e_w)
+    return (vals, meta, e_w, mask) if want_mask else (vals, meta, e_w)
+
+
+def compress_fp8(W: torch.Tensor, mask: torch.Tensor):
+    """The same conversion under a given 2:4 mask: (vals, meta, e_w)."""
+    N, K = W.shape
+    vals, meta, e_w = _alloc_fp8_weight(N, K, W.device)
+    _b.sp24_compress_fp8(W, mask, vals, meta, e_w)
+    return vals, meta, e_w
+
+
+def gemm_fp8(X: torch.Tensor, e_x: torch.Tensor, vals: torch.Tensor, meta: torch.Tensor,
+             e_w: torch.Tensor, N: int, out_kind: int = _b.SP24_OUT_BF16,
+             out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Y [M, N] = X W'^T of e4m3 activations (X, e_x) and a converted weight
+    (vals, meta, e_w); bf16 or (SP24_OUT_F32) float32."""
+    if out is None:
+        odt = torch.float32 if out_kind == _b.SP24_OUT_F32 else torch.bfloat16
+        out = torch.empty((X.shape[0], N), dtype=odt, device=X.device)
+    _b.sp24_gemm_fp8(X, e_x, vals, meta, e_w, N, out_kind, out)
+    return out
+
+
+class RmsNorm(NamedTuple):
+    y: torch.Tensor                  # e4m3, int8 or bf16 [M, K]
+    e_y: Optional[torch.Tensor]      # e8m0 scales of an e4m3 output
+    h: torch.Tensor                  # x + residual as stored (x itself without one)
+    rstd: Optional[torch.Tensor]     # float32 [M] when asked for
+
+
+_NORM_TORCH = {_b.SP24_FP8: torch.float8_e4m3fn, _b.SP24_INT8: torch.int8,
+               _b.SP24_BF16: torch.bfloat16}
+
+
+def rmsnorm_quant(X: torch.Tensor, gamma: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                  eps: float = 1e-6, out_dtype: int = _b.SP24_FP8,
+                  s_x: Optional[torch.Tensor] = None, want_rstd: bool = False,
+                  out: Optional[torch.Tensor] = None, out_scales: Optional[torch.Tensor] = None,
+                  out_sum: Optional[torch.Tensor] = None) -> RmsNorm:
+    """RMS norm of X (+ residual) with the next product's operand as its output:
+    e4m3 with block scales (for gemm_fp8), int8 with the given scale s_x (for
+    gemm) or bf16.  out_sum may be X or residual: the stream updated in place."""
+    M, K = X.shape
+    if out is None:
+        out = torch.empty((M, K), dtype=_NORM_TORCH[out_dtype], device=X.device)
+    if out_dtype != _b.SP24_FP8:
+        out_scales = None
+    elif out_scales is None:
+        out_scales = _scales(M, K, X.device)
+    if out_sum is None and residual is not None:
+        out_sum = torch.empty_like(X)
+    rstd = torch.empty(M, dtype=torch.float32, device=X.device) if want_rstd else None
+    _b.sp24_rmsnorm_quant(X, residual, gamma, eps, out_dtype, s_x, out_sum, out, out_scales, rstd)
+    return RmsNorm(out, out_scales, X if out_sum is None else out_sum, rstd)
+
+
+def rmsnorm_backward(dY: torch.Tensor, H: torch.Tensor, gamma: torch.Tensor, rstd: torch.Tensor,
+                     dH: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(dX, dgamma float32) of rmsnorm_quant, the 8-bit rounding passed straight
+    through: dY is the gradient of y, H and rstd come from the forward call and
+    dH is the gradient that reaches H past the norm."""
+    M, K = H.shape
+    if out is None:
+        out = torch.empty_like(H)
+    if workspace is None:
+        workspace = torch.empty(_b.sp24_rmsnorm_backward_workspace_bytes(M, K), dtype=torch.uint8,
+                                device=H.device)
+    dgamma = torch.empty(K, dtype=torch.float32, device=H.device)
+    _b.sp24_rmsnorm_backward(dY, dH, H, gamma, rstd, out, dgamma, workspace)
+    return out, dgamma
 
 
 def fake_quant(W: torch.Tensor, mask: torch.Tensor, s_w: torch.Tensor) -> torch.Tensor:

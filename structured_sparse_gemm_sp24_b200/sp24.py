@@ -30,9 +30,13 @@ SP24_MAGNITUDE = 0
 SP24_WANDA = 1
 SP24_BF16 = 0
 SP24_INT8 = 1
+SP24_FP8 = 2
+SP24_F32 = 3
 SP24_OUT_BF16 = 0
 SP24_OUT_INT32 = 1
 SP24_OUT_INT8 = 2
+SP24_OUT_F32 = 3
+SP24_NORM_MAX_K = 16384
 SP24_NOALLOC_MAX_K = 65536
 SP24_PERMUTE_MAX_K = 65536
 
@@ -41,6 +45,7 @@ _c_p = ctypes.c_void_p
 _c_int = ctypes.c_int
 _c_dbl = ctypes.c_double
 _c_size = ctypes.c_size_t
+_c_flt = ctypes.c_float
 
 # name -> (restype, argtypes)
 SIGNATURES = {
@@ -79,6 +84,18 @@ SIGNATURES = {
     "sp24_permute_search": (_c_int, [_c_p, _c_i64, _c_i64, _c_p, _c_int, _c_i64, _c_p, _c_p,
                                      _c_size, _c_p, _c_p]),
     "sp24_permute_columns": (_c_int, [_c_p, _c_i64, _c_i64, _c_int, _c_p, _c_p, _c_p]),
+    "sp24_scale_bytes": (_c_size, [_c_i64, _c_i64]),
+    "sp24_quantize_fp8": (_c_int, [_c_p, _c_i64, _c_i64, _c_int, _c_p, _c_p, _c_p]),
+    "sp24_prune_compress_fp8": (_c_int, [_c_p, _c_i64, _c_i64, _c_int, _c_p, _c_p, _c_p, _c_p,
+                                         _c_p, _c_p, _c_p]),
+    "sp24_compress_fp8": (_c_int, [_c_p, _c_p, _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_p]),
+    "sp24_gemm_fp8": (_c_int, [_c_p, _c_p, _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_i64, _c_int,
+                               _c_p, _c_p]),
+    "sp24_rmsnorm_quant": (_c_int, [_c_p, _c_p, _c_p, _c_i64, _c_i64, _c_int, _c_flt, _c_int,
+                                    _c_p, _c_p, _c_p, _c_p, _c_p, _c_p]),
+    "sp24_rmsnorm_backward_workspace_bytes": (_c_size, [_c_i64, _c_i64]),
+    "sp24_rmsnorm_backward": (_c_int, [_c_p, _c_p, _c_p, _c_p, _c_p, _c_i64, _c_i64, _c_int, _c_p,
+                                       _c_p, _c_p, _c_size, _c_p]),
     "sp24_im2col3x3": (_c_int, [_c_p, _c_i64, _c_i64, _c_i64, _c_i64, _c_int, _c_p, _c_p]),
 }
 
@@ -161,6 +178,37 @@ def _stream(stream) -> Optional[int]:
     return int(stream)
 
 
+# Element types of the e4m3 and norm entry points (whose tensors are checked:
+# a wrong type or size would be read as another).
+_CODE_OF = {torch.bfloat16: SP24_BF16, torch.float32: SP24_F32}
+_FP8 = (torch.float8_e4m3fn,)
+_SCALE = (torch.float8_e8m0fnu, torch.uint8)
+
+
+def _arg(t: Optional[torch.Tensor], name: str, dtypes, numel: int, dev: int):
+    """Pointer of a dense CUDA tensor of one of `dtypes` with `numel` elements on
+    device `dev`; None stays None."""
+    if t is None:
+        return None
+    if not t.is_cuda or t.get_device() != dev:
+        raise ValueError(f"sp24: {name} must be a CUDA tensor on the current device ({dev})")
+    if t.dtype not in dtypes:
+        raise ValueError(f"sp24: {name} has type {t.dtype}, expected one of {dtypes}")
+    if t.numel() != numel or not t.is_contiguous():
+        raise ValueError(f"sp24: {name} must be contiguous with {numel} elements")
+    return t.data_ptr()
+
+
+def _matrix(t: torch.Tensor, name: str):
+    if t.dim() != 2:
+        raise ValueError(f"sp24: {name} must be a matrix, got {tuple(t.shape)}")
+    return t.shape
+
+
+def _scale_cols(K: int) -> int:
+    return 4 * ((K + 511) // 512)
+
+
 # ------------------------------------------------------------------- sizes
 def sp24_mask_bytes(N: int, K: int) -> int:
     return lib().sp24_mask_bytes(N, K)
@@ -176,6 +224,14 @@ def sp24_meta_bytes(N: int, K: int) -> int:
 
 def sp24_prune_workspace_bytes(K: int, mode: int) -> int:
     return lib().sp24_prune_workspace_bytes(K, mode)
+
+
+def sp24_scale_bytes(rows: int, K: int) -> int:
+    return lib().sp24_scale_bytes(rows, K)
+
+
+def sp24_rmsnorm_backward_workspace_bytes(M: int, K: int) -> int:
+    return lib().sp24_rmsnorm_backward_workspace_bytes(M, K)
 
 
 def sp24_act_scale_workspace_bytes() -> int:
@@ -325,6 +381,100 @@ def sp24_im2col3x3(X: torch.Tensor, A: torch.Tensor, stream=None) -> None:
     Bn, H, W, C = X.shape
     _check(lib().sp24_im2col3x3(_ptr(X), Bn, H, W, C, X.element_size(), _ptr(A),
                                 _stream(stream)), "sp24_im2col3x3")
+
+
+def sp24_quantize_fp8(X: torch.Tensor, Xq: torch.Tensor, e_x: torch.Tensor, stream=None) -> None:
+    """X bf16 or float32 [M, K] -> e4m3 codes [M, K] and e8m0 scales."""
+    M, K = _matrix(X, "X")
+    dev, n = torch.cuda.current_device(), X.numel()
+    _check(lib().sp24_quantize_fp8(
+        _arg(X, "X", _CODE_OF, n, dev), M, K, _CODE_OF.get(X.dtype, -1),
+        _arg(Xq, "Xq", _FP8, n, dev), _arg(e_x, "e_x", _SCALE, M * _scale_cols(K), dev),
+        _stream(stream)), "sp24_quantize_fp8")
+
+
+def sp24_prune_compress_fp8(W: torch.Tensor, mode: int, norms: Optional[torch.Tensor],
+                            mask_in: Optional[torch.Tensor], mask_out: Optional[torch.Tensor],
+                            vals: torch.Tensor, meta: torch.Tensor, e_w: torch.Tensor,
+                            stream=None) -> None:
+    N, K = _matrix(W, "W")
+    dev, mb = torch.cuda.current_device(), N * (K // 8)
+    _check(lib().sp24_prune_compress_fp8(
+        _arg(W, "W", (torch.bfloat16,), N * K, dev), N, K, mode,
+        _arg(norms, "norms", (torch.float64,), K, dev),
+        _arg(mask_in, "mask_in", (torch.uint8,), mb, dev),
+        _arg(mask_out, "mask_out", (torch.uint8,), mb, dev),
+        _arg(vals, "vals", _FP8, N * (K // 2), dev),
+        _arg(meta, "meta", (torch.uint8,), _meta_numel(meta, N, K), dev),
+        _arg(e_w, "e_w", _SCALE, (N + 127) // 128 * _scale_cols(K), dev),
+        _stream(stream)), "sp24_prune_compress_fp8")
+
+
+def sp24_compress_fp8(W: torch.Tensor, mask: torch.Tensor, vals: torch.Tensor,
+                      meta: torch.Tensor, e_w: torch.Tensor, stream=None) -> None:
+    N, K = _matrix(W, "W")
+    dev = torch.cuda.current_device()
+    _check(lib().sp24_compress_fp8(
+        _arg(W, "W", (torch.bfloat16,), N * K, dev),
+        _arg(mask, "mask", (torch.uint8,), N * (K // 8), dev), N, K,
+        _arg(vals, "vals", _FP8, N * (K // 2), dev),
+        _arg(meta, "meta", (torch.uint8,), _meta_numel(meta, N, K), dev),
+        _arg(e_w, "e_w", _SCALE, (N + 127) // 128 * _scale_cols(K), dev),
+        _stream(stream)), "sp24_compress_fp8")
+
+
+def _meta_numel(meta: torch.Tensor, N: int, K: int) -> int:
+    """Elements expected of a metadata tensor: at least the layout's bytes (an
+    allocation may be larger)."""
+    return max((N + 127) // 128 * ((K + 127) // 128) * 2048, meta.numel())
+
+
+def sp24_gemm_fp8(X: torch.Tensor, e_x: torch.Tensor, vals: torch.Tensor, meta: torch.Tensor,
+                  e_w: torch.Tensor, N: int, out_kind: int, Y: torch.Tensor, stream=None) -> None:
+    """Y [M, N] = X W'^T of e4m3 X [M, K] and a compressed e4m3 weight."""
+    M, K = _matrix(X, "X")
+    dev = torch.cuda.current_device()
+    ydt = torch.float32 if out_kind == SP24_OUT_F32 else torch.bfloat16
+    _check(lib().sp24_gemm_fp8(
+        _arg(X, "X", _FP8, M * K, dev), _arg(e_x, "e_x", _SCALE, M * _scale_cols(K), dev), M, K,
+        _arg(vals, "vals", _FP8, N * (K // 2), dev),
+        _arg(meta, "meta", (torch.uint8,), _meta_numel(meta, N, K), dev),
+        _arg(e_w, "e_w", _SCALE, (N + 127) // 128 * _scale_cols(K), dev), N, out_kind,
+        _arg(Y, "Y", (ydt,), M * N, dev), _stream(stream)), "sp24_gemm_fp8")
+
+
+_NORM_OUT = {SP24_FP8: _FP8, SP24_INT8: (torch.int8,), SP24_BF16: (torch.bfloat16,)}
+
+
+def sp24_rmsnorm_quant(X: torch.Tensor, R: Optional[torch.Tensor], gamma: torch.Tensor, eps: float,
+                       out_dtype: int, s_x: Optional[torch.Tensor], H: Optional[torch.Tensor],
+                       Y: torch.Tensor, e_y: Optional[torch.Tensor],
+                       rstd: Optional[torch.Tensor], stream=None) -> None:
+    """RMS norm of X (+ R) with an e4m3, int8 or bf16 output."""
+    M, K = _matrix(X, "X")
+    dev, n, dt = torch.cuda.current_device(), X.numel(), (X.dtype,)
+    _check(lib().sp24_rmsnorm_quant(
+        _arg(X, "X", _CODE_OF, n, dev), _arg(R, "R", dt, n, dev), _arg(gamma, "gamma", dt, K, dev),
+        M, K, _CODE_OF.get(X.dtype, -1), eps, out_dtype,
+        _arg(s_x, "s_x", (torch.float32,), 1, dev), _arg(H, "H", dt, n, dev),
+        _arg(Y, "Y", _NORM_OUT.get(out_dtype, ()), n, dev),
+        _arg(e_y, "e_y", _SCALE, M * _scale_cols(K), dev),
+        _arg(rstd, "rstd", (torch.float32,), M, dev), _stream(stream)), "sp24_rmsnorm_quant")
+
+
+def sp24_rmsnorm_backward(dY: torch.Tensor, dH: Optional[torch.Tensor], H: torch.Tensor,
+                          gamma: torch.Tensor, rstd: torch.Tensor, dX: torch.Tensor,
+                          dgamma: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
+    """Gradients of sp24_rmsnorm_quant to X (and R) and gamma."""
+    M, K = _matrix(H, "H")
+    dev, n, dt = torch.cuda.current_device(), H.numel(), (H.dtype,)
+    _check(lib().sp24_rmsnorm_backward(
+        _arg(dY, "dY", dt, n, dev), _arg(dH, "dH", dt, n, dev), _arg(H, "H", _CODE_OF, n, dev),
+        _arg(gamma, "gamma", dt, K, dev), _arg(rstd, "rstd", (torch.float32,), M, dev), M, K,
+        _CODE_OF.get(H.dtype, -1), _arg(dX, "dX", dt, n, dev),
+        _arg(dgamma, "dgamma", (torch.float32,), K, dev),
+        _arg(workspace, "workspace", (torch.uint8,), workspace.numel(), dev),
+        workspace.numel(), _stream(stream)), "sp24_rmsnorm_backward")
 
 
 def sp24_selftest_wait_timeout(limit_ns: int, stream=None) -> None:
