@@ -35,7 +35,7 @@ constexpr int kEpiBox = 32;              // channels per warp store box
 constexpr int kConvProducerWarp = 2 + kEpiWarps;
 __host__ __device__ constexpr int gemm_threads(bool conv) { return 64 + kEpiThreads + (conv ? 64 : 0); }
 
-// The e4m3 product adds the same two warps: warp 10 lays out its block scales.
+// The e4m3 product adds two warps as well: warps 10 and 11 lay out its scales.
 constexpr int kScaleWarp = 2 + kEpiWarps;
 
 template <int OUTK>

@@ -23,8 +23,7 @@
 
 namespace sp24 {
 
-// kBuf: scale buffers in tensor memory (the copy of the next word may then
-// run while MMAs still read the current one).
+// kBuf: scale buffers in tensor memory.
 template <int kDtype, int BN, int kBuf>
 struct SfCfg {
   static constexpr bool kOn = kDtype == SP24_FP8;

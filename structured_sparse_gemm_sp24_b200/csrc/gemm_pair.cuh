@@ -19,9 +19,18 @@
 //    empty: the even CTA's barrier collects one arrival per epilogue warp of
 //    both CTAs.
 // Warps: 0 = TMA producer (both CTAs), 1 = MMA issuer (even CTA), 2..9 =
-// epilogue (both CTAs; warp 2 also owns the tensor-memory allocation), 10 (e4m3
-// only) = block scales (both CTAs: each needs the scales of all BN tokens and
-// of its own weight rows in its tensor memory).
+// epilogue (both CTAs; warp 2 also owns the tensor-memory allocation), 10 and 11
+// (e4m3 only) = block scales (both CTAs: each needs the scales of all BN tokens
+// and of its own weight rows in its tensor memory).
+// The scales have a ring of their own, two stages to a word, so that their
+// longer way (loads, shared-memory stores, a release to the even CTA) runs ahead
+// of the MMAs; their copies to tensor memory cost the MMAs nothing measurable
+// (resident operands: 502 cycles a stage with them, 494 without).
+//
+// One thread issues everything the tensor pipe does, so its instructions bound
+// the kernel unless they are few: 8192 x 4096 x 4096 int8 took 70 us with
+// descriptors built from scratch for each MMA by the thread `lane == 0`, 66 us
+// with the arithmetic below, and 62 us once the thread was chosen by elect.sync.
 #pragma once
 
 namespace sp24 {
@@ -40,9 +49,8 @@ struct PairCfg {
   static constexpr int kMetaCols = 4 * kMetaChunks;
   static constexpr int kAcc = ACC;
   static constexpr int kMetaCol0 = kAcc * BN;
-  // e4m3: as many scale buffers (two at most) as tensor memory has room for
-  static constexpr int kSfCol0 = kAcc * BN + 2 * kMetaCols;
-  using Sf = SfCfg<kDtype, BN, (512 - kSfCol0 >= 2 * SfCfg<kDtype, BN, 1>::kBufCols ? 2 : 1)>;
+  static constexpr int kSfCol0 = kAcc * BN + 2 * kMetaCols;      // e4m3: the scales
+  using Sf = SfCfg<kDtype, BN, 1>;
   static constexpr int kTmemNeeded = kSfCol0 + Sf::kCols;
   static constexpr int kTmemCols = kTmemNeeded <= 32 ? 32
                                    : kTmemNeeded <= 64 ? 64
@@ -51,10 +59,11 @@ struct PairCfg {
   static constexpr int kOutBytes = EpiOut<OUTK>::kBytes;
   static constexpr int kStagingBytes = EpiOut<OUTK>::kStagingBytes;  // all epilogue warps
   static constexpr int kRingBytes = STAGES * kStageStride;
-  // scale buffers in shared memory: as many as stages, so a buffer's next load
-  // event comes at least STAGES iterations after the copy that reads it
-  static constexpr int kSfBytes = STAGES * Sf::kSmemBuf;
-  static constexpr int kSmemBytes = kRingBytes + kStagingBytes + kSfBytes + 1024 + 256;
+  static constexpr int kSfBufs = 4;   // scale words in shared memory (2 stages each)
+  static constexpr int kSfBytes = kSfBufs * Sf::kSmemBuf;
+  static constexpr int kBarBytes = (2 * STAGES + 2 * kAcc + (Sf::kOn ? 3 * kSfBufs : 0)) * 8 + 16;
+  static constexpr int kSmemBytes =
+      kRingBytes + kStagingBytes + kSfBytes + 1024 + (kBarBytes + 255) / 256 * 256;
   static_assert(kTmemNeeded <= 512, "tensor memory overflow");
   static_assert(BN % 16 == 0 && BN >= 64 && BN <= 256, "BN");
   static_assert(kSmemBytes <= 232448, "shared memory");
@@ -84,7 +93,10 @@ gemm_sp_pair(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
   uint64_t* empty_bar = full_bar + STAGES;
   uint64_t* tfull_bar = empty_bar + STAGES;
   uint64_t* tempty_bar = tfull_bar + C::kAcc;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty_bar + C::kAcc);
+  uint64_t* sfull_bar = tempty_bar + C::kAcc;       // scale ring (e4m3)
+  uint64_t* sempty_bar = sfull_bar + (C::Sf::kOn ? C::kSfBufs : 0);
+  uint64_t* slocal_bar = sempty_bar + (C::Sf::kOn ? C::kSfBufs : 0);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(slocal_bar + (C::Sf::kOn ? C::kSfBufs : 0));
   volatile uint32_t* abort_flag = tmem_slot + 1;
 
   const int warp = threadIdx.x >> 5;
@@ -97,12 +109,19 @@ gemm_sp_pair(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&full_bar[s], C::Sf::kOn ? 3 : 1);   // producer (and both scale loaders)
+      mbar_init(&full_bar[s], 1);
       mbar_init(&empty_bar[s], 1);
     }
     for (int a = 0; a < C::kAcc; ++a) {
       mbar_init(&tfull_bar[a], 1);
       mbar_init(&tempty_bar[a], 2 * kEpiWarps);   // epilogue warps of both CTAs
+    }
+    if constexpr (C::Sf::kOn) {
+      for (int b = 0; b < C::kSfBufs; ++b) {
+        mbar_init(&sfull_bar[b], 2);    // both CTAs' forwarding warps
+        mbar_init(&sempty_bar[b], 1);
+        mbar_init(&slocal_bar[b], 1);   // this CTA's loader
+      }
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -118,7 +137,7 @@ gemm_sp_pair(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
   pdl_wait_prior();   // set-up above overlapped the previous kernel's tail
 
   if (warp == 0 || (kConv && warp == kConvProducerWarp)) {
-    if (lane == 0) {
+    if (elect_one()) {
       // -------------------------------------------------------- producer
       // (the implicit convolution runs two producer warps, each loading every
       // other stage: its token loads take longer to issue)
@@ -171,67 +190,91 @@ gemm_sp_pair(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0 && elect_one()) {
       // ------------------------------------------------------ MMA issuer
-      uint32_t it = 0, j = 0;
-      uint32_t sf_n = 0, sf_col = 0;   // scale loads so far, their current columns
-      for (int tile = pair; tile < ntiles && !*abort_flag; tile += npairs, ++j) {
-        const uint32_t acc = j % C::kAcc;
-        if (!mbar_wait(&tempty_bar[acc], ((j / C::kAcc) & 1u) ^ 1u)) { *abort_flag = 1; break; }
+      // One thread feeds the tensor pipe, so its own instructions per MMA are
+      // on the critical path: slot and phase advance by addition, descriptors
+      // are a constant high word and a low word (address / 16) moved by
+      // constants, and only a tile's last stage counts its MMAs.
+      uint32_t s = 0, ph = 0, meta_buf = 0, acc = 0, acc_ph = 0;
+      const uint32_t ring = smem_u32(smem) >> 4;
+      uint32_t st = ring;                                   // slot's address / 16
+      const int last_kb = args.kblocks - 1;
+      const int last_mmas = static_cast<int>(
+          (args.k - static_cast<int64_t>(last_kb) * C::kLogicalK + C::kMmaK - 1) / C::kMmaK);
+      constexpr uint32_t kAbHi = desc_hi(1024, kSwizzle128B);
+      uint32_t sf_buf = 0, sf_ph = 0;                       // e4m3: the next scale word
+      bool ok = true;
+      for (int tile = pair; ok && tile < ntiles && !*abort_flag; tile += npairs) {
+        if (!mbar_wait(&tempty_bar[acc], acc_ph ^ 1u)) { ok = false; break; }
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * BN;
-        bool aborted = false;
-        for (int kb = 0; kb < args.kblocks; ++kb, ++it) {
-          const int s = it % STAGES;
-          const uint32_t ph = (it / STAGES) & 1u;
-          if (!mbar_wait(&full_bar[s], ph)) { *abort_flag = 1; aborted = true; break; }
-          if constexpr (C::Sf::kOn) fence_acquire_cluster();   // the peer's scales
-          tc_fence_after();
-          uint8_t* st = smem + s * C::kStageStride;
-          const uint32_t a_addr = smem_u32(st);
-          const uint32_t b_addr = smem_u32(st + C::kABytes);
-          const uint32_t e_addr = smem_u32(st + C::kABytes + 2 * C::kBHalfBytes);
-          const uint32_t meta_col = C::kMetaCol0 + (it & 1u) * C::kMetaCols;
-          const int64_t k_left = args.k - static_cast<int64_t>(kb) * C::kLogicalK;
-          int n_mma = static_cast<int>((k_left + C::kMmaK - 1) / C::kMmaK);
-          n_mma = n_mma > 4 ? 4 : n_mma;
-          for (int c = 0; c < C::kMetaChunks; ++c)
-            tc_cp_128x128b_pair(tmem_base + meta_col + 4 * c,
-                                smem_desc(e_addr + 2048 * c, 128, 128, kSwizzleNone));
+        uint32_t accumulate = 0;
+        for (int kb = 0; kb <= last_kb; ++kb) {
+          if (!mbar_wait(&full_bar[s], ph)) { ok = false; break; }
           if constexpr (C::Sf::kOn) {
-            if (sf_load_stage(kb, 0)) {
-              sf_col = tmem_base + C::kSfCol0 + (sf_n % C::Sf::kBufs) * C::Sf::kBufCols;
-              sf_copy<typename C::Sf, true>(sf_col,
-                                            smem_u32(sf_smem) + (sf_n % STAGES) * C::Sf::kSmemBuf);
-              ++sf_n;
-            }
+            // (cluster scope: the peer's warps wrote its scales)
+            if ((kb & 1) == 0 && !mbar_wait_cluster(&sfull_bar[sf_buf], sf_ph)) { ok = false; break; }
           }
+          tc_fence_after();
+          const uint32_t meta_col = tmem_base + C::kMetaCol0 + meta_buf * C::kMetaCols;
+          const uint32_t e_lo = st + (C::kABytes + 2 * C::kBHalfBytes) / 16;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            if (q < n_mma) {
-              const uint64_t a_desc = smem_desc(a_addr + 32 * q, 0, 1024, kSwizzle128B);
-              const uint64_t b_desc = smem_desc(
-                  b_addr + (q >> 1) * C::kBHalfBytes + 64 * (q & 1), 0, 1024, kSwizzle128B);
-              const uint32_t accumulate = (kb > 0 || q > 0) ? 1u : 0u;
-              if constexpr (kDtype == SP24_BF16) {
-                tc_mma_sp_pair(d_tmem, a_desc, b_desc, tmem_base + meta_col + (q & ~1),
-                               make_idesc_pair<kDtype, BN>(q & 1), accumulate);
-              } else if constexpr (kDtype == SP24_FP8) {
-                // byte of the scale word: this MMA's 128-position block mod 4
-                tc_mma_sp_fp8_pair(d_tmem, a_desc, b_desc, tmem_base + meta_col + 2 * q,
-                                   make_idesc_fp8<BN>(256, (kb & 1) * 2 + (q >> 1)),
-                                   sf_col + 4 * C::Sf::kTiles, sf_col, accumulate);
-              } else {
-                tc_mma_sp_i8_pair(d_tmem, a_desc, b_desc, tmem_base + meta_col + 2 * q,
-                                  make_idesc_pair<kDtype, BN>(0), accumulate);
+          for (int c = 0; c < C::kMetaChunks; ++c)
+            tc_cp_128x128b_pair(meta_col + 4 * c, desc_of(e_lo + 128 * c + (8u << 16),
+                                                          desc_hi(128, kSwizzleNone)));
+          if constexpr (C::Sf::kOn) {
+            if ((kb & 1) == 0) {
+              sf_copy<typename C::Sf, true>(tmem_base + C::kSfCol0,
+                                            smem_u32(sf_smem) + sf_buf * C::Sf::kSmemBuf);
+              tc_commit_pair_mc(&sempty_bar[sf_buf], 0x3);
+              if (++sf_buf == C::kSfBufs) {
+                sf_buf = 0;
+                sf_ph ^= 1u;
               }
             }
           }
+          const int n_mma = kb == last_kb ? last_mmas : 4;
+          const uint32_t b_lo = st + C::kABytes / 16;
+          // (e4m3) byte of the scale word: the MMA's 128-position block mod 4
+          const uint32_t sf_byte = (kb & 1) * 2;
+          constexpr uint32_t kSfB = C::kSfCol0, kSfA = C::kSfCol0 + 4 * C::Sf::kTiles;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            if (q < n_mma) {
+              const uint64_t a_desc = desc_of(st + 2 * q, kAbHi);
+              const uint64_t b_desc =
+                  desc_of(b_lo + (q >> 1) * (C::kBHalfBytes / 16) + 4 * (q & 1), kAbHi);
+              if constexpr (kDtype == SP24_BF16) {
+                tc_mma_sp_pair(d_tmem, a_desc, b_desc, meta_col + (q & ~1),
+                               make_idesc_pair<kDtype, BN>(q & 1), accumulate);
+              } else if constexpr (kDtype == SP24_FP8) {
+                tc_mma_sp_fp8_pair(d_tmem, a_desc, b_desc, meta_col + 2 * q,
+                                   make_idesc_fp8<BN>(256, sf_byte + (q >> 1)),
+                                   tmem_base + kSfA, tmem_base + kSfB, accumulate);
+              } else {
+                tc_mma_sp_i8_pair(d_tmem, a_desc, b_desc, meta_col + 2 * q,
+                                  make_idesc_pair<kDtype, BN>(0), accumulate);
+              }
+              accumulate = 1;
+            }
+          }
           tc_commit_pair_mc(&empty_bar[s], 0x3);   // frees the stage in both CTAs
+          meta_buf ^= 1u;
+          st += C::kStageStride / 16;
+          if (++s == STAGES) {
+            s = 0;
+            ph ^= 1u;
+            st = ring;
+          }
         }
         tc_commit_pair_mc(&tfull_bar[acc], 0x3);   // both epilogues may drain
-        if (aborted) break;
+        if (++acc == C::kAcc) {
+          acc = 0;
+          acc_ph ^= 1u;
+        }
       }
+      if (!ok) *abort_flag = 1;
     }
   } else if (warp < 2 + kEpiWarps) {
     // --------------------------------------------------------- epilogue
@@ -269,32 +312,61 @@ gemm_sp_pair(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
     if (lane == 0) bulk_wait<0>();
   } else if (C::Sf::kOn && warp == kScaleWarp) {
     // ----------------------------------------------------- scale loader
+    // Words in the order the MMA thread takes them, two of them in flight.
     if constexpr (C::Sf::kOn) {
-      uint32_t it = 0, sf_n = 0;
-      SfWords<BN> words;
       const int64_t row_tiles128 = (args.n + 127) / 128;
-      for (int tile = pair; tile < ntiles && !*abort_flag; tile += npairs) {
+      const int words_per_tile = (args.kblocks + 1) / 2;
+      SfWords<BN> w0, w1;
+      uint32_t j = 0;             // word to store next
+      int tile = pair, word = 0;  // word to load next
+      auto load = [&](SfWords<BN>& w) {
+        if (tile >= ntiles) return;
         int prt, tt;
         tile_coords(tile, args, prt, tt);
-        const int64_t rt128 = prt * 2 + static_cast<int>(rank);
-        const int64_t tok0 = static_cast<int64_t>(tt) * BN;
-        words.load(args.e_x, args.e_w, args.sf_words, 0, tok0, args.m, rt128, row_tiles128, lane);
+        w.load(args.e_x, args.e_w, args.sf_words, word, static_cast<int64_t>(tt) * BN, args.m,
+               prt * 2 + static_cast<int>(rank), row_tiles128, lane);
+        if (++word == words_per_tile) { word = 0; tile += npairs; }
+      };
+      const uint32_t all =
+          pair < ntiles ? static_cast<uint32_t>((ntiles - pair + npairs - 1) / npairs) *
+                              static_cast<uint32_t>(words_per_tile)
+                        : 0u;
+      auto put = [&](SfWords<BN>& w) -> bool {
+        const uint32_t b = j % C::kSfBufs;
         bool ok = true;
-        for (int kb = 0; kb < args.kblocks; ++kb, ++it) {
-          const int s = it % STAGES;
-          if (lane == 0) ok = mbar_wait(&empty_bar[s], ((it / STAGES) & 1u) ^ 1u);
-          ok = __shfl_sync(0xffffffffu, ok, 0);
-          if (!ok) { *abort_flag = 1; break; }
-          if (sf_load_stage(kb, 0)) {
-            words.store(sf_smem + (sf_n % STAGES) * C::Sf::kSmemBuf, lane);
-            ++sf_n;
-            if (kb + 2 < args.kblocks)
-              words.load(args.e_x, args.e_w, args.sf_words, kb / 2 + 1, tok0, args.m, rt128,
-                         row_tiles128, lane);
+        if (lane == 0) ok = !*abort_flag && mbar_wait(&sempty_bar[b], ((j / C::kSfBufs) & 1u) ^ 1u);
+        if (!__shfl_sync(0xffffffffu, ok, 0)) { *abort_flag = 1; return false; }
+        w.store(sf_smem + b * C::Sf::kSmemBuf, lane);
+        if (lane == 0) mbar_arrive(&slocal_bar[b]);
+        ++j;
+        load(w);
+        return true;
+      };
+      load(w0);
+      load(w1);
+      while (j < all) {
+        if (!put(w0)) break;
+        if (j < all && !put(w1)) break;
+      }
+    }
+  } else if (C::Sf::kOn && warp == kScaleWarp + 1) {
+    // -------------------------------------------------- scale forwarder
+    // Hands this CTA's words on to the even CTA.  A release at cluster scope
+    // waits for the thread's loads in flight, so the loader does not make it.
+    if constexpr (C::Sf::kOn) {
+      if (lane == 0) {
+        const uint32_t words_per_tile = static_cast<uint32_t>(args.kblocks + 1) / 2;
+        const uint32_t all =
+            pair < ntiles ? static_cast<uint32_t>((ntiles - pair + npairs - 1) / npairs) * words_per_tile
+                          : 0u;
+        for (uint32_t j = 0; j < all; ++j) {
+          const uint32_t b = j % C::kSfBufs;
+          if (*abort_flag || !mbar_wait(&slocal_bar[b], (j / C::kSfBufs) & 1u)) {
+            *abort_flag = 1;
+            break;
           }
-          if (lane == 0) mbar_arrive_release_cluster(map_peer(smem_u32(&full_bar[s]), 0));
+          mbar_arrive_release_cluster(map_peer(smem_u32(&sfull_bar[b]), 0));
         }
-        if (!ok) break;
       }
     }
   }

@@ -313,7 +313,7 @@ sp24_status dispatch(const void* x, const void* vals, GemmArgs a, cudaStream_t s
                     static_cast<uint64_t>(a.n), box_cols, 128));
   const int pairs = static_cast<int>(p.ctas / 2);
   if constexpr (kDtype == SP24_FP8) {
-    // one stage fewer at 256 tokens (and 32-bit output): the scale buffers
+    // one stage fewer at 256 tokens (and with 32-bit output): the scale buffers
     switch (p.impl) {
       case kPair256: return launch_pair_out<kDtype, 256, 3, 3, 1>(ma, a, x, pairs, s);
       case kPair240: return launch_pair_out<kDtype, 240, 4, 3, 2>(ma, a, x, pairs, s);

@@ -42,6 +42,20 @@ __device__ __forceinline__ void pdl_wait_prior() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// True in one lane of a converged warp.  Single-thread sections that issue
+// tcgen05 or TMA instructions are entered by it and not by `lane == 0`: the
+// compiler then knows that one lane is active, and the uniform operands of
+// those instructions need no loop over possibly different lanes.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
@@ -300,6 +314,15 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo_bytes
   return d;
 }
 
+// The same descriptor from its two words: lo = address / 16 (+ leading offset /
+// 16 << 16), hi = stride offset, version and swizzle.  Shared-memory addresses
+// are below 2^18, so address / 16 stays in its 14 bits.
+constexpr __host__ __device__ uint32_t desc_hi(uint32_t sbo_bytes, uint32_t swizzle) {
+  return (sbo_bytes >> 4) | (1u << 14) | (swizzle << 29);
+}
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo, uint32_t hi) {
+  return (static_cast<uint64_t>(hi) << 32) | lo;
+}
 
 // ------------------------------------------------------- TMA store / groups
 // 2D tiled tensor store from this CTA's shared memory (bulk-group completion).
@@ -517,10 +540,30 @@ __device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t bar_cluster
                ::"r"(bar_cluster) : "memory");
 }
 
-// Orders what the phase that just completed on an mbarrier released at cluster
-// scope before this thread's later accesses.
-__device__ __forceinline__ void fence_acquire_cluster() {
-  asm volatile("fence.acq_rel.cluster;" ::: "memory");
+// mbar_wait that acquires at cluster scope: what threads of other CTAs released
+// with their arrivals is visible afterwards.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity) {
+  if (mbar_try_wait_cluster(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      raise_error(kErrTimeoutBit);
+      return false;
+    }
+  }
 }
 
 // ------------------------------------------------------------------ cluster
