@@ -18,7 +18,7 @@
 // store; the MMA thread copies the tile with tcgen05.cp (the four lane
 // quadrants get the same data).  A weight tile's 128 rows share one word: its
 // tile is 8 rows of 16 bytes that the copy reads four times (row-group stride
-// 0).  Words are loaded every other stage, one stage ahead in registers.
+// 0).
 #pragma once
 
 namespace sp24 {
@@ -38,38 +38,63 @@ struct SfCfg {
 // Whether stage kb of a K range starting at kb0 begins a scale word.
 __device__ __forceinline__ bool sf_load_stage(int kb, int kb0) { return kb == kb0 || (kb & 1) == 0; }
 
-// The loader warp's words of one tile: tokens tok0 + lane + 32 j and the
-// tile's weight row block.
-template <int BN>
+// A loader warp's words of one tile: words word0 .. word0 + G - 1 of the tokens
+// tok0 + lane + 32 j and of the tile's weight row block.
+template <int BN, int G>
 struct SfWords {
   static constexpr int kRows = (BN + 31) / 32;
-  uint32_t x[kRows];
-  uint32_t w;
+  uint32_t x[kRows][G];
+  uint32_t w[G];
 
-  // Word `word` of the rows; rows past the ends read as scale 1 (their
-  // accumulator columns and lanes are not stored).
+  // Words past the row (word0 + g >= words) and rows past the ends read as
+  // scale 1 (their accumulator columns and lanes are not stored).  With G = 4
+  // and rows of whole 16-byte pieces one load fetches the four words.
   __device__ __forceinline__ void load(const uint32_t* e_x, const uint32_t* e_w, int64_t words,
-                                       int64_t word, int64_t tok0, int64_t m, int64_t rt,
+                                       int64_t word0, int64_t tok0, int64_t m, int64_t rt,
                                        int64_t row_tiles, int lane) {
+    const bool vec = G == 4 && (words & 3) == 0;
 #pragma unroll
     for (int j = 0; j < kRows; ++j) {
       const int64_t t = tok0 + 32 * j + lane;
-      x[j] = (t < m && 32 * j + lane < BN) ? __ldg(e_x + t * words + word) : 0x7F7F7F7Fu;
+      const bool ok = t < m && 32 * j + lane < BN;
+      fetch(x[j], e_x + t * words + word0, ok, vec, words - word0);
     }
-    w = rt < row_tiles ? __ldg(e_w + rt * words + word) : 0x7F7F7F7Fu;
+    fetch(w, e_w + rt * words + word0, rt < row_tiles, vec, words - word0);
   }
 
-  // Writes the tiles of one scale buffer (weight tile, then token tiles).
-  __device__ __forceinline__ void store(uint8_t* buf, int lane) const {
-    if (lane < 8) *reinterpret_cast<uint4*>(buf + 16 * lane) = make_uint4(w, w, w, w);
+  __device__ __forceinline__ static void fetch(uint32_t (&d)[G], const uint32_t* p, bool ok, bool vec,
+                                               int64_t left) {
+    if constexpr (G == 4) {
+      if (vec) {
+        const uint4 q = ok ? __ldg(reinterpret_cast<const uint4*>(p))
+                           : make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+        d[0] = q.x;
+        d[1] = q.y;
+        d[2] = q.z;
+        d[3] = q.w;
+        return;
+      }
+    }
 #pragma unroll
-    for (int t = 0; t < (kRows + 3) / 4; ++t) {
-      uint4 v;
-      v.x = x[4 * t];
-      v.y = 4 * t + 1 < kRows ? x[4 * t + 1 < kRows ? 4 * t + 1 : 0] : 0x7F7F7F7Fu;
-      v.z = 4 * t + 2 < kRows ? x[4 * t + 2 < kRows ? 4 * t + 2 : 0] : 0x7F7F7F7Fu;
-      v.w = 4 * t + 3 < kRows ? x[4 * t + 3 < kRows ? 4 * t + 3 : 0] : 0x7F7F7F7Fu;
-      *reinterpret_cast<uint4*>(buf + 128 + 512 * t + 16 * lane) = v;
+    for (int g = 0; g < G; ++g) d[g] = ok && g < left ? __ldg(p + g) : 0x7F7F7F7Fu;
+  }
+
+  // Writes the tiles of the words, one scale buffer after another (each the
+  // weight tile, then the token tiles).
+  __device__ __forceinline__ void store(uint8_t* buf, int buf_bytes, int lane) const {
+#pragma unroll
+    for (int g = 0; g < G; ++g, buf += buf_bytes) {
+      if (lane < 8) *reinterpret_cast<uint4*>(buf + 16 * lane) = make_uint4(w[g], w[g], w[g], w[g]);
+#pragma unroll
+      for (int t = 0; t < (kRows + 3) / 4; ++t) {
+        uint32_t v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int j = 4 * t + i < kRows ? 4 * t + i : 0;
+          v[i] = 4 * t + i < kRows ? x[j][g] : 0x7F7F7F7Fu;
+        }
+        *reinterpret_cast<uint4*>(buf + 128 + 512 * t + 16 * lane) = make_uint4(v[0], v[1], v[2], v[3]);
+      }
     }
     fence_async_shared();
     __syncwarp();

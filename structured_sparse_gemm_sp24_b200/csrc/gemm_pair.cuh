@@ -59,9 +59,11 @@ struct PairCfg {
   static constexpr int kOutBytes = EpiOut<OUTK>::kBytes;
   static constexpr int kStagingBytes = EpiOut<OUTK>::kStagingBytes;  // all epilogue warps
   static constexpr int kRingBytes = STAGES * kStageStride;
-  static constexpr int kSfBufs = 4;   // scale words in shared memory (2 stages each)
+  // scale words in shared memory (2 stages each): a group of four for either
+  // loader warp
+  static constexpr int kSfBufs = 8;
   static constexpr int kSfBytes = kSfBufs * Sf::kSmemBuf;
-  static constexpr int kBarBytes = (2 * STAGES + 2 * kAcc + (Sf::kOn ? 3 * kSfBufs : 0)) * 8 + 16;
+  static constexpr int kBarBytes = (2 * STAGES + 2 * kAcc + (Sf::kOn ? 4 : 0)) * 8 + 16;
   static constexpr int kSmemBytes =
       kRingBytes + kStagingBytes + kSfBytes + 1024 + (kBarBytes + 255) / 256 * 256;
   static_assert(kTmemNeeded <= 512, "tensor memory overflow");
@@ -94,9 +96,8 @@ gemm_sp_pair(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
   uint64_t* tfull_bar = empty_bar + STAGES;
   uint64_t* tempty_bar = tfull_bar + C::kAcc;
   uint64_t* sfull_bar = tempty_bar + C::kAcc;       // scale ring (e4m3)
-  uint64_t* sempty_bar = sfull_bar + (C::Sf::kOn ? C::kSfBufs : 0);
-  uint64_t* slocal_bar = sempty_bar + (C::Sf::kOn ? C::kSfBufs : 0);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(slocal_bar + (C::Sf::kOn ? C::kSfBufs : 0));
+  uint64_t* sempty_bar = sfull_bar + (C::Sf::kOn ? 2 : 0);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sempty_bar + (C::Sf::kOn ? 2 : 0));
   volatile uint32_t* abort_flag = tmem_slot + 1;
 
   const int warp = threadIdx.x >> 5;
@@ -117,10 +118,9 @@ gemm_sp_pair(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
       mbar_init(&tempty_bar[a], 2 * kEpiWarps);   // epilogue warps of both CTAs
     }
     if constexpr (C::Sf::kOn) {
-      for (int b = 0; b < C::kSfBufs; ++b) {
-        mbar_init(&sfull_bar[b], 2);    // both CTAs' forwarding warps
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&sfull_bar[b], 2);    // the warp in either CTA
         mbar_init(&sempty_bar[b], 1);
-        mbar_init(&slocal_bar[b], 1);   // this CTA's loader
       }
     }
     *abort_flag = 0;
@@ -203,7 +203,7 @@ gemm_sp_pair(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
       const int last_mmas = static_cast<int>(
           (args.k - static_cast<int64_t>(last_kb) * C::kLogicalK + C::kMmaK - 1) / C::kMmaK);
       constexpr uint32_t kAbHi = desc_hi(1024, kSwizzle128B);
-      uint32_t sf_buf = 0, sf_ph = 0;                       // e4m3: the next scale word
+      uint32_t sf_ring = 0, sf_ph = 0;   // e4m3: the current group's loader, its phase
       bool ok = true;
       for (int tile = pair; ok && tile < ntiles && !*abort_flag; tile += npairs) {
         if (!mbar_wait(&tempty_bar[acc], acc_ph ^ 1u)) { ok = false; break; }
@@ -214,7 +214,7 @@ gemm_sp_pair(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
           if (!mbar_wait(&full_bar[s], ph)) { ok = false; break; }
           if constexpr (C::Sf::kOn) {
             // (cluster scope: the peer's warps wrote its scales)
-            if ((kb & 1) == 0 && !mbar_wait_cluster(&sfull_bar[sf_buf], sf_ph)) { ok = false; break; }
+            if ((kb & 7) == 0 && !mbar_wait_cluster(&sfull_bar[sf_ring], sf_ph)) { ok = false; break; }
           }
           tc_fence_after();
           const uint32_t meta_col = tmem_base + C::kMetaCol0 + meta_buf * C::kMetaCols;
@@ -225,13 +225,15 @@ gemm_sp_pair(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
                                                           desc_hi(128, kSwizzleNone)));
           if constexpr (C::Sf::kOn) {
             if ((kb & 1) == 0) {
+              const int slot = 4 * sf_ring + ((kb >> 1) & 3);
               sf_copy<typename C::Sf, true>(tmem_base + C::kSfCol0,
-                                            smem_u32(sf_smem) + sf_buf * C::Sf::kSmemBuf);
-              tc_commit_pair_mc(&sempty_bar[sf_buf], 0x3);
-              if (++sf_buf == C::kSfBufs) {
-                sf_buf = 0;
-                sf_ph ^= 1u;
-              }
+                                            smem_u32(sf_smem) + slot * C::Sf::kSmemBuf);
+              // the group's last word
+              if ((kb & 7) == 6 || kb >= last_kb - 1) tc_commit_pair_mc(&sempty_bar[sf_ring], 0x3);
+            }
+            if ((kb & 7) == 7 || kb == last_kb) {   // the group's last stage
+              sf_ph ^= sf_ring;
+              sf_ring ^= 1u;
             }
           }
           const int n_mma = kb == last_kb ? last_mmas : 4;
@@ -310,63 +312,37 @@ gemm_sp_pair(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
       });
     }
     if (lane == 0) bulk_wait<0>();
-  } else if (C::Sf::kOn && warp == kScaleWarp) {
-    // ----------------------------------------------------- scale loader
-    // Words in the order the MMA thread takes them, two of them in flight.
+  } else if (C::Sf::kOn && warp >= kScaleWarp) {
+    // ---------------------------------------------------- scale loaders
+    // The words of a tile in groups of four (one 16-byte load a token), every
+    // other group to each of the two warps.  A group is handed over as a whole:
+    // the release at cluster scope takes 1000 cycles and more (it waits for the
+    // thread's accesses in flight), which a release a word, or the next loads
+    // before it, put on the critical path (8192 x 4096 x 4096: 73 and 125 us).
     if constexpr (C::Sf::kOn) {
-      const int64_t row_tiles128 = (args.n + 127) / 128;
-      const int words_per_tile = (args.kblocks + 1) / 2;
-      SfWords<BN> w0, w1;
-      uint32_t j = 0;             // word to store next
-      int tile = pair, word = 0;  // word to load next
-      auto load = [&](SfWords<BN>& w) {
-        if (tile >= ntiles) return;
+      const int ring = warp - kScaleWarp;
+      const int groups = (args.kblocks + 7) / 8;          // per tile
+      int tile = pair, group = ring;                      // this warp's next group
+      uint32_t bph = 0;
+      uint8_t* buf = sf_smem + ring * 4 * C::Sf::kSmemBuf;
+      while (true) {
+        while (group >= groups && tile < ntiles) {
+          group -= groups;
+          tile += npairs;
+        }
+        if (tile >= ntiles) break;
         int prt, tt;
         tile_coords(tile, args, prt, tt);
-        w.load(args.e_x, args.e_w, args.sf_words, word, static_cast<int64_t>(tt) * BN, args.m,
-               prt * 2 + static_cast<int>(rank), row_tiles128, lane);
-        if (++word == words_per_tile) { word = 0; tile += npairs; }
-      };
-      const uint32_t all =
-          pair < ntiles ? static_cast<uint32_t>((ntiles - pair + npairs - 1) / npairs) *
-                              static_cast<uint32_t>(words_per_tile)
-                        : 0u;
-      auto put = [&](SfWords<BN>& w) -> bool {
-        const uint32_t b = j % C::kSfBufs;
+        SfWords<BN, 4> words;
+        words.load(args.e_x, args.e_w, args.sf_words, 4 * group, static_cast<int64_t>(tt) * BN,
+                   args.m, prt * 2 + static_cast<int>(rank), (args.n + 127) / 128, lane);
         bool ok = true;
-        if (lane == 0) ok = !*abort_flag && mbar_wait(&sempty_bar[b], ((j / C::kSfBufs) & 1u) ^ 1u);
-        if (!__shfl_sync(0xffffffffu, ok, 0)) { *abort_flag = 1; return false; }
-        w.store(sf_smem + b * C::Sf::kSmemBuf, lane);
-        if (lane == 0) mbar_arrive(&slocal_bar[b]);
-        ++j;
-        load(w);
-        return true;
-      };
-      load(w0);
-      load(w1);
-      while (j < all) {
-        if (!put(w0)) break;
-        if (j < all && !put(w1)) break;
-      }
-    }
-  } else if (C::Sf::kOn && warp == kScaleWarp + 1) {
-    // -------------------------------------------------- scale forwarder
-    // Hands this CTA's words on to the even CTA.  A release at cluster scope
-    // waits for the thread's loads in flight, so the loader does not make it.
-    if constexpr (C::Sf::kOn) {
-      if (lane == 0) {
-        const uint32_t words_per_tile = static_cast<uint32_t>(args.kblocks + 1) / 2;
-        const uint32_t all =
-            pair < ntiles ? static_cast<uint32_t>((ntiles - pair + npairs - 1) / npairs) * words_per_tile
-                          : 0u;
-        for (uint32_t j = 0; j < all; ++j) {
-          const uint32_t b = j % C::kSfBufs;
-          if (*abort_flag || !mbar_wait(&slocal_bar[b], (j / C::kSfBufs) & 1u)) {
-            *abort_flag = 1;
-            break;
-          }
-          mbar_arrive_release_cluster(map_peer(smem_u32(&sfull_bar[b]), 0));
-        }
+        if (lane == 0) ok = !*abort_flag && mbar_wait(&sempty_bar[ring], bph ^ 1u);
+        if (!__shfl_sync(0xffffffffu, ok, 0)) { *abort_flag = 1; break; }
+        words.store(buf, C::Sf::kSmemBuf, lane);
+        if (lane == 0) mbar_arrive_release_cluster(map_peer(smem_u32(&sfull_bar[ring]), 0));
+        bph ^= 1u;
+        group += 2;
       }
     }
   }

@@ -187,7 +187,7 @@ gemm_sp_kernel(const __grid_constant__ CUtensorMap tmap_a,
     // -------------------------------------------------------- scale loader
     if constexpr (C::Sf::kOn) {
       uint32_t sf_n = 0;
-      SfWords<BN> words;
+      SfWords<BN, 1> words;
       const int64_t tok0 = tok_tile * BN;
       if (n_iters > 0)
         words.load(args.e_x, args.e_w, args.sf_words, kb_begin / 2, tok0, args.m, row_tile,
@@ -199,7 +199,7 @@ gemm_sp_kernel(const __grid_constant__ CUtensorMap tmap_a,
         if (lane == 0) ok = mbar_wait(&empty_bar[s], ((i / STAGES) & 1u) ^ 1u);
         if (!__shfl_sync(0xffffffffu, ok, 0)) { *abort_flag = 1; break; }
         if (sf_load_stage(kb, kb_begin)) {
-          words.store(smem + STAGES * C::kStageStride + (sf_n % C::kSfBufs) * C::Sf::kSmemBuf, lane);
+          words.store(smem + STAGES * C::kStageStride + (sf_n % C::kSfBufs) * C::Sf::kSmemBuf, 0, lane);
           ++sf_n;
           const int next = kb / 2 + 1;
           if (2 * next < kb_end)
