@@ -133,7 +133,9 @@ gemm_sp_pair(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
   tc_fence_before();
   cluster_sync();          // barriers of both CTAs initialised before any remote use
   tc_fence_after();
-  const uint32_t tmem_base = *tmem_slot;
+  // an allocation of all 512 columns starts at 0, which keeps the addresses
+  // constants of the issuing thread
+  const uint32_t tmem_base = C::kTmemCols == 512 ? 0u : *tmem_slot;
   pdl_wait_prior();   // set-up above overlapped the previous kernel's tail
 
   if (warp == 0 || (kConv && warp == kConvProducerWarp)) {
@@ -195,7 +197,8 @@ gemm_sp_pair(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
       // One thread feeds the tensor pipe, so its own instructions per MMA are
       // on the critical path: slot and phase advance by addition, descriptors
       // are a constant high word and a low word (address / 16) moved by
-      // constants, and only a tile's last stage counts its MMAs.
+      // constants, only a tile's last stage counts its MMAs, and the next
+      // slot's barrier is asked before this stage's MMAs are issued.
       uint32_t s = 0, ph = 0, meta_buf = 0, acc = 0, acc_ph = 0;
       const uint32_t ring = smem_u32(smem) >> 4;
       uint32_t st = ring;                                   // slot's address / 16
@@ -205,13 +208,13 @@ gemm_sp_pair(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
       constexpr uint32_t kAbHi = desc_hi(1024, kSwizzle128B);
       uint32_t sf_ring = 0, sf_ph = 0;   // e4m3: the current group's loader, its phase
       bool ok = true;
+      bool ready = false;                // slot s is known to be full
       for (int tile = pair; ok && tile < ntiles && !*abort_flag; tile += npairs) {
         if (!mbar_wait(&tempty_bar[acc], acc_ph ^ 1u)) { ok = false; break; }
-        tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * BN;
         uint32_t accumulate = 0;
         for (int kb = 0; kb <= last_kb; ++kb) {
-          if (!mbar_wait(&full_bar[s], ph)) { ok = false; break; }
+          if (!ready && !mbar_wait(&full_bar[s], ph)) { ok = false; break; }
           if constexpr (C::Sf::kOn) {
             // (cluster scope: the peer's warps wrote its scales)
             if ((kb & 7) == 0 && !mbar_wait_cluster(&sfull_bar[sf_ring], sf_ph)) { ok = false; break; }
@@ -236,39 +239,44 @@ gemm_sp_pair(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
               sf_ring ^= 1u;
             }
           }
-          const int n_mma = kb == last_kb ? last_mmas : 4;
           const uint32_t b_lo = st + C::kABytes / 16;
-          // (e4m3) byte of the scale word: the MMA's 128-position block mod 4
-          const uint32_t sf_byte = (kb & 1) * 2;
-          constexpr uint32_t kSfB = C::kSfCol0, kSfA = C::kSfCol0 + 4 * C::Sf::kTiles;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            if (q < n_mma) {
-              const uint64_t a_desc = desc_of(st + 2 * q, kAbHi);
-              const uint64_t b_desc =
-                  desc_of(b_lo + (q >> 1) * (C::kBHalfBytes / 16) + 4 * (q & 1), kAbHi);
-              if constexpr (kDtype == SP24_BF16) {
-                tc_mma_sp_pair(d_tmem, a_desc, b_desc, meta_col + (q & ~1),
-                               make_idesc_pair<kDtype, BN>(q & 1), accumulate);
-              } else if constexpr (kDtype == SP24_FP8) {
-                tc_mma_sp_fp8_pair(d_tmem, a_desc, b_desc, meta_col + 2 * q,
-                                   make_idesc_fp8<BN>(256, sf_byte + (q >> 1)),
-                                   tmem_base + kSfA, tmem_base + kSfB, accumulate);
-              } else {
-                tc_mma_sp_i8_pair(d_tmem, a_desc, b_desc, meta_col + 2 * q,
-                                  make_idesc_pair<kDtype, BN>(0), accumulate);
-              }
-              accumulate = 1;
+          auto mma = [&](int q) {
+            const uint64_t a_desc = desc_of(st + 2 * q, kAbHi);
+            const uint64_t b_desc =
+                desc_of(b_lo + (q >> 1) * (C::kBHalfBytes / 16) + 4 * (q & 1), kAbHi);
+            if constexpr (kDtype == SP24_BF16) {
+              tc_mma_sp_pair(d_tmem, a_desc, b_desc, meta_col + (q & ~1),
+                             make_idesc_pair<kDtype, BN>(q & 1), accumulate);
+            } else if constexpr (kDtype == SP24_FP8) {
+              // byte of the scale word: the MMA's 128-position block mod 4
+              tc_mma_sp_fp8_pair(d_tmem, a_desc, b_desc, meta_col + 2 * q,
+                                 make_idesc_fp8<BN>(256, (kb & 1) * 2 + (q >> 1)),
+                                 tmem_base + C::kSfCol0 + 4 * C::Sf::kTiles, tmem_base + C::kSfCol0,
+                                 accumulate);
+            } else {
+              tc_mma_sp_i8_pair(d_tmem, a_desc, b_desc, meta_col + 2 * q,
+                                make_idesc_pair<kDtype, BN>(0), accumulate);
             }
-          }
-          tc_commit_pair_mc(&empty_bar[s], 0x3);   // frees the stage in both CTAs
-          meta_buf ^= 1u;
-          st += C::kStageStride / 16;
+            accumulate = 1;
+          };
+          const uint32_t s_now = s;
+          mma(0);
           if (++s == STAGES) {
             s = 0;
             ph ^= 1u;
-            st = ring;
           }
+          ready = mbar_try_wait(&full_bar[s], ph);
+          if (kb != last_kb || last_mmas == 4) {
+            mma(1);
+            mma(2);
+            mma(3);
+          } else {
+            if (last_mmas > 1) mma(1);
+            if (last_mmas > 2) mma(2);
+          }
+          tc_commit_pair_mc(&empty_bar[s_now], 0x3);   // frees the stage in both CTAs
+          meta_buf ^= 1u;
+          st = s == 0 ? ring : st + C::kStageStride / 16;
         }
         tc_commit_pair_mc(&tfull_bar[acc], 0x3);   // both epilogues may drain
         if (++acc == C::kAcc) {

@@ -56,7 +56,6 @@ __global__ void __launch_bounds__(128, 1)
 gemm_sp_kernel(const __grid_constant__ CUtensorMap tmap_a,
                const __grid_constant__ CUtensorMap tmap_b, const GemmArgs args) {
   pdl_launch_dependents();
-  pdl_wait_prior();
   using C = GemmCfg<kDtype, BN, STAGES>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -94,95 +93,109 @@ gemm_sp_kernel(const __grid_constant__ CUtensorMap tmap_a,
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  pdl_wait_prior();   // set-up above overlapped the previous kernel's tail
 
-  if (warp == 0 && lane == 0) {
-    // ------------------------------------------------------------ producer
-    prefetch_tmap(&tmap_a);
-    prefetch_tmap(&tmap_b);
-    const int kchunks = static_cast<int>((args.k + 127) / 128);
-    const uint8_t* meta_tile = args.meta + row_tile * static_cast<int64_t>(kchunks) * 2048;
-    for (int i = 0; i < n_iters; ++i) {
-      const int s = i % STAGES;
-      const uint32_t ph = (i / STAGES) & 1u;
-      if (!mbar_wait(&empty_bar[s], ph ^ 1u)) { *abort_flag = 1; break; }
-      const int kb = kb_begin + i;
-      uint8_t* st = smem + s * C::kStageStride;
-      int chunks = C::kMetaChunks;
-      if (C::kMetaChunks == 2 && 2 * kb + 1 >= kchunks) chunks = 1;
-      mbar_arrive_expect_tx(&full_bar[s], C::kABytes + 2 * C::kBHalfBytes + 2048 * chunks);
-      // A: compressed columns [kb*128B) of rows [row_tile*128, +128)
-      tma_load_2d(st, &tmap_a, &full_bar[s], kb * (kDtype == SP24_BF16 ? 64 : 128),
-                  static_cast<int32_t>(row_tile * 128));
-      // B: logical K [kb*KL, +KL) of tokens [tok_tile*BN, +BN), two halves
-      const int kx = kb * C::kLogicalK;
-      const int half = C::kLogicalK / 2;
-      tma_load_2d(st + C::kABytes, &tmap_b, &full_bar[s], kx,
-                  static_cast<int32_t>(tok_tile * BN));
-      tma_load_2d(st + C::kABytes + C::kBHalfBytes, &tmap_b, &full_bar[s], kx + half,
-                  static_cast<int32_t>(tok_tile * BN));
-      // E: metadata chunk(s) of this K block
-      const int c0 = kb * C::kMetaChunks;
-      bulk_load(st + C::kABytes + 2 * C::kBHalfBytes, meta_tile + static_cast<int64_t>(c0) * 2048,
-                2048u * chunks, &full_bar[s]);
+  if (warp == 0) {
+    if (elect_one()) {
+      // ------------------------------------------------------------ producer
+      prefetch_tmap(&tmap_a);
+      prefetch_tmap(&tmap_b);
+      const int kchunks = static_cast<int>((args.k + 127) / 128);
+      const uint8_t* meta_tile = args.meta + row_tile * static_cast<int64_t>(kchunks) * 2048;
+      for (int i = 0; i < n_iters; ++i) {
+        const int s = i % STAGES;
+        const uint32_t ph = (i / STAGES) & 1u;
+        if (!mbar_wait(&empty_bar[s], ph ^ 1u)) { *abort_flag = 1; break; }
+        const int kb = kb_begin + i;
+        uint8_t* st = smem + s * C::kStageStride;
+        int chunks = C::kMetaChunks;
+        if (C::kMetaChunks == 2 && 2 * kb + 1 >= kchunks) chunks = 1;
+        mbar_arrive_expect_tx(&full_bar[s], C::kABytes + 2 * C::kBHalfBytes + 2048 * chunks);
+        // A: compressed columns [kb*128B) of rows [row_tile*128, +128)
+        tma_load_2d(st, &tmap_a, &full_bar[s], kb * (kDtype == SP24_BF16 ? 64 : 128),
+                    static_cast<int32_t>(row_tile * 128));
+        // B: logical K [kb*KL, +KL) of tokens [tok_tile*BN, +BN), two halves
+        const int kx = kb * C::kLogicalK;
+        const int half = C::kLogicalK / 2;
+        tma_load_2d(st + C::kABytes, &tmap_b, &full_bar[s], kx,
+                    static_cast<int32_t>(tok_tile * BN));
+        tma_load_2d(st + C::kABytes + C::kBHalfBytes, &tmap_b, &full_bar[s], kx + half,
+                    static_cast<int32_t>(tok_tile * BN));
+        // E: metadata chunk(s) of this K block
+        const int c0 = kb * C::kMetaChunks;
+        bulk_load(st + C::kABytes + 2 * C::kBHalfBytes, meta_tile + static_cast<int64_t>(c0) * 2048,
+                  2048u * chunks, &full_bar[s]);
+      }
     }
-  } else if (warp == 1 && lane == 0) {
-    // ---------------------------------------------------------- MMA issuer
-    const int64_t k_total = args.k;
-    uint32_t sf_n = 0, sf_col = 0;   // scale loads so far, their current columns
-    for (int i = 0; i < n_iters; ++i) {
-      const int s = i % STAGES;
-      const uint32_t ph = (i / STAGES) & 1u;
-      if (!mbar_wait(&full_bar[s], ph)) { *abort_flag = 1; break; }
-      tc_fence_after();
-      const int kb = kb_begin + i;
-      uint8_t* st = smem + s * C::kStageStride;
-      const uint32_t a_addr = smem_u32(st);
-      const uint32_t b_addr = smem_u32(st + C::kABytes);
-      const uint32_t e_addr = smem_u32(st + C::kABytes + 2 * C::kBHalfBytes);
-      const uint32_t meta_col = C::kMetaCol0 + (i & 1) * C::kMetaCols;
-      // MMAs that touch real K positions in this stage (the tail stage may
-      // need fewer; the rest would only multiply zero fill)
-      const int64_t k_left = k_total - static_cast<int64_t>(kb) * C::kLogicalK;
-      int n_mma = static_cast<int>((k_left + C::kMmaK - 1) / C::kMmaK);
-      n_mma = n_mma > 4 ? 4 : n_mma;
-      const int chunks = kDtype == SP24_BF16 ? 1 : (n_mma > 2 ? 2 : 1);
-      for (int c = 0; c < chunks; ++c) {
-        // 128 rows x 16 bytes, rows contiguous: core matrices of 8 rows at 128 B
-        tc_cp_128x128b(tmem_base + meta_col + 4 * c,
-                       smem_desc(e_addr + 2048 * c, 128, 128, kSwizzleNone));
-      }
-      if constexpr (C::Sf::kOn) {
-        if (sf_load_stage(kb, kb_begin)) {
-          sf_col = tmem_base + C::kSfCol0 + (sf_n % C::Sf::kBufs) * C::Sf::kBufCols;
-          sf_copy<typename C::Sf, false>(
-              sf_col, smem_u32(smem + STAGES * C::kStageStride) + (sf_n % C::kSfBufs) * C::Sf::kSmemBuf);
-          ++sf_n;
-        }
-      }
+  } else if (warp == 1) {
+    if (elect_one()) {
+      // ---------------------------------------------------------- MMA issuer
+      // (few instructions per MMA, as in the CTA-pair kernel: at few tokens an
+      // MMA takes about as long as its issue)
+      uint32_t sf_n = 0, sf_col = 0;   // scale loads so far, their current columns
+      uint32_t s = 0, ph = 0;
+      const uint32_t ring = smem_u32(smem) >> 4;
+      uint32_t st = ring;              // slot's address / 16
+      constexpr uint32_t kAbHi = desc_hi(1024, kSwizzle128B);
+      // MMAs that touch real K positions in the whole K's last stage (the rest
+      // would only multiply zero fill)
+      const int last_kb = args.kblocks - 1;
+      const int last_mmas = static_cast<int>(
+          (args.k - static_cast<int64_t>(last_kb) * C::kLogicalK + C::kMmaK - 1) / C::kMmaK);
+      uint32_t accumulate = 0;
+      for (int i = 0; i < n_iters; ++i) {
+        if (!mbar_wait(&full_bar[s], ph)) { *abort_flag = 1; break; }
+        tc_fence_after();
+        const int kb = kb_begin + i;
+        const uint32_t e_lo = st + (C::kABytes + 2 * C::kBHalfBytes) / 16 + (8u << 16);
+        const uint32_t meta_col = tmem_base + C::kMetaCol0 + (i & 1) * C::kMetaCols;
+        const int n_mma = kb == last_kb ? last_mmas : 4;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (j < n_mma) {
-          const uint64_t a_desc = smem_desc(a_addr + 32 * j, 0, 1024, kSwizzle128B);
-          const uint64_t b_desc =
-              smem_desc(b_addr + (j >> 1) * C::kBHalfBytes + 64 * (j & 1), 0, 1024, kSwizzle128B);
-          const uint32_t accumulate = (i > 0 || j > 0) ? 1u : 0u;
-          if constexpr (kDtype == SP24_BF16) {
-            tc_mma_sp(tmem_base, a_desc, b_desc, tmem_base + meta_col + (j & ~1),
-                      make_idesc<kDtype, BN>(j & 1), accumulate);
-          } else if constexpr (kDtype == SP24_FP8) {
-            // byte of the scale word: this MMA's 128-position block mod 4
-            tc_mma_sp_fp8(tmem_base, a_desc, b_desc, tmem_base + meta_col + 2 * j,
-                          make_idesc_fp8<BN>(128, (kb & 1) * 2 + (j >> 1)),
-                          sf_col + 4 * C::Sf::kTiles, sf_col, accumulate);
-          } else {
-            tc_mma_sp_i8(tmem_base, a_desc, b_desc, tmem_base + meta_col + 2 * j,
-                         make_idesc<kDtype, BN>(0), accumulate);
+        for (int c = 0; c < C::kMetaChunks; ++c) {
+          // 128 rows x 16 bytes, rows contiguous: core matrices of 8 rows at 128 B
+          if (c == 0 || n_mma > 2)
+            tc_cp_128x128b(meta_col + 4 * c, desc_of(e_lo + 128 * c, desc_hi(128, kSwizzleNone)));
+        }
+        if constexpr (C::Sf::kOn) {
+          if (sf_load_stage(kb, kb_begin)) {
+            sf_col = tmem_base + C::kSfCol0 + (sf_n % C::Sf::kBufs) * C::Sf::kBufCols;
+            sf_copy<typename C::Sf, false>(
+                sf_col, smem_u32(smem + STAGES * C::kStageStride) + (sf_n % C::kSfBufs) * C::Sf::kSmemBuf);
+            ++sf_n;
           }
         }
+        const uint32_t b_lo = st + C::kABytes / 16;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (j < n_mma) {
+            const uint64_t a_desc = desc_of(st + 2 * j, kAbHi);
+            const uint64_t b_desc =
+                desc_of(b_lo + (j >> 1) * (C::kBHalfBytes / 16) + 4 * (j & 1), kAbHi);
+            if constexpr (kDtype == SP24_BF16) {
+              tc_mma_sp(tmem_base, a_desc, b_desc, meta_col + (j & ~1),
+                        make_idesc<kDtype, BN>(j & 1), accumulate);
+            } else if constexpr (kDtype == SP24_FP8) {
+              // byte of the scale word: this MMA's 128-position block mod 4
+              tc_mma_sp_fp8(tmem_base, a_desc, b_desc, meta_col + 2 * j,
+                            make_idesc_fp8<BN>(128, (kb & 1) * 2 + (j >> 1)),
+                            sf_col + 4 * C::Sf::kTiles, sf_col, accumulate);
+            } else {
+              tc_mma_sp_i8(tmem_base, a_desc, b_desc, meta_col + 2 * j,
+                           make_idesc<kDtype, BN>(0), accumulate);
+            }
+            accumulate = 1;
+          }
+        }
+        tc_commit(&empty_bar[s]);   // frees the stage once these MMAs are done
+        st += C::kStageStride / 16;
+        if (++s == STAGES) {
+          s = 0;
+          ph ^= 1u;
+          st = ring;
+        }
       }
-      tc_commit(&empty_bar[s]);   // frees the stage once these MMAs are done
+      tc_commit(accum_bar);         // accumulator complete
     }
-    tc_commit(accum_bar);         // accumulator complete
   } else if (C::Sf::kOn && warp == 3) {
     // -------------------------------------------------------- scale loader
     if constexpr (C::Sf::kOn) {

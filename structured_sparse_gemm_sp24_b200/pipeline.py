@@ -125,8 +125,8 @@ def gemm(X: torch.Tensor, vals: torch.Tensor, meta: torch.Tensor, N: int,
     return out
 
 
-def _scales(rows: int, K: int, device) -> torch.Tensor:
-    return torch.empty((rows, 4 * ((K + 511) // 512)), dtype=torch.float8_e8m0fnu, device=device)
+def _scales(rows: int, K: int, like: torch.Tensor) -> torch.Tensor:
+    return like.new_empty((rows, 4 * ((K + 511) // 512)), dtype=torch.float8_e8m0fnu)
 
 
 def quantize_fp8(X: torch.Tensor, out: Optional[torch.Tensor] = None,
@@ -135,17 +135,17 @@ def quantize_fp8(X: torch.Tensor, out: Optional[torch.Tensor] = None,
     blocks of 128 columns [M, 4 * ceil(K / 512)] (columns past the last block: 1)."""
     M, K = X.shape
     if out is None:
-        out = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=X.device)
+        out = X.new_empty((M, K), dtype=torch.float8_e4m3fn)
     if out_scales is None:
-        out_scales = _scales(M, K, X.device)
+        out_scales = _scales(M, K, X)
     _b.sp24_quantize_fp8(X, out, out_scales)
     return out, out_scales
 
 
-def _alloc_fp8_weight(N: int, K: int, device):
-    return (torch.empty((N, K // 2), dtype=torch.float8_e4m3fn, device=device),
-            torch.empty(_b.sp24_meta_bytes(N, K), dtype=torch.uint8, device=device),
-            _scales((N + 127) // 128, K, device))
+def _alloc_fp8_weight(N: int, K: int, like: torch.Tensor):
+    return (like.new_empty((N, K // 2), dtype=torch.float8_e4m3fn),
+            like.new_empty(_b.sp24_meta_bytes(N, K), dtype=torch.uint8),
+            _scales((N + 127) // 128, K, like))
 
 
 def prune_compress_fp8(W: torch.Tensor, mode: int = _b.SP24_MAGNITUDE,
@@ -154,8 +154,8 @@ def prune_compress_fp8(W: torch.Tensor, mode: int = _b.SP24_MAGNITUDE,
     """e4m3 weight conversion in one pass: (vals e4m3 [N, K/2], meta, e_w[, mask])
     with one e8m0 scale per 128 x 128 block."""
     N, K = W.shape
-    vals, meta, e_w = _alloc_fp8_weight(N, K, W.device)
-    mask = torch.empty((N, K // 8), dtype=torch.uint8, device=W.device) if want_mask else None
+    vals, meta, e_w = _alloc_fp8_weight(N, K, W)
+    mask = W.new_empty((N, K // 8), dtype=torch.uint8) if want_mask else None
     _b.sp24_prune_compress_fp8(W, mode, norms, mask_in, mask, vals, meta, e_w)
     return (vals, meta, e_w, mask) if want_mask else (vals, meta, e_w)
 
@@ -163,7 +163,7 @@ def prune_compress_fp8(W: torch.Tensor, mode: int = _b.SP24_MAGNITUDE,
 def compress_fp8(W: torch.Tensor, mask: torch.Tensor):
     """The same conversion under a given 2:4 mask: (vals, meta, e_w)."""
     N, K = W.shape
-    vals, meta, e_w = _alloc_fp8_weight(N, K, W.device)
+    vals, meta, e_w = _alloc_fp8_weight(N, K, W)
     _b.sp24_compress_fp8(W, mask, vals, meta, e_w)
     return vals, meta, e_w
 
@@ -175,7 +175,7 @@ def gemm_fp8(X: torch.Tensor, e_x: torch.Tensor, vals: torch.Tensor, meta: torch
     (vals, meta, e_w); bf16 or (SP24_OUT_F32) float32."""
     if out is None:
         odt = torch.float32 if out_kind == _b.SP24_OUT_F32 else torch.bfloat16
-        out = torch.empty((X.shape[0], N), dtype=odt, device=X.device)
+        out = X.new_empty((X.shape[0], N), dtype=odt)
     _b.sp24_gemm_fp8(X, e_x, vals, meta, e_w, N, out_kind, out)
     return out
 
@@ -201,14 +201,14 @@ def rmsnorm_quant(X: torch.Tensor, gamma: torch.Tensor, residual: Optional[torch
     gemm) or bf16.  out_sum may be X or residual: the stream updated in place."""
     M, K = X.shape
     if out is None:
-        out = torch.empty((M, K), dtype=_NORM_TORCH[out_dtype], device=X.device)
+        out = X.new_empty((M, K), dtype=_NORM_TORCH[out_dtype])
     if out_dtype != _b.SP24_FP8:
         out_scales = None
     elif out_scales is None:
-        out_scales = _scales(M, K, X.device)
+        out_scales = _scales(M, K, X)
     if out_sum is None and residual is not None:
         out_sum = torch.empty_like(X)
-    rstd = torch.empty(M, dtype=torch.float32, device=X.device) if want_rstd else None
+    rstd = X.new_empty(M, dtype=torch.float32) if want_rstd else None
     _b.sp24_rmsnorm_quant(X, residual, gamma, eps, out_dtype, s_x, out_sum, out, out_scales, rstd)
     return RmsNorm(out, out_scales, X if out_sum is None else out_sum, rstd)
 
@@ -223,9 +223,8 @@ def rmsnorm_backward(dY: torch.Tensor, H: torch.Tensor, gamma: torch.Tensor, rst
     if out is None:
         out = torch.empty_like(H)
     if workspace is None:
-        workspace = torch.empty(_b.sp24_rmsnorm_backward_workspace_bytes(M, K), dtype=torch.uint8,
-                                device=H.device)
-    dgamma = torch.empty(K, dtype=torch.float32, device=H.device)
+        workspace = H.new_empty(_b.sp24_rmsnorm_backward_workspace_bytes(M, K), dtype=torch.uint8)
+    dgamma = H.new_empty(K, dtype=torch.float32)
     _b.sp24_rmsnorm_backward(dY, dH, H, gamma, rstd, out, dgamma, workspace)
     return out, dgamma
 

@@ -171,8 +171,8 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _stream(stream) -> Optional[int]:
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:   # (current_stream() builds a Python object: 3 us a call)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -190,11 +190,12 @@ def _arg(t: Optional[torch.Tensor], name: str, dtypes, numel: int, dev: int):
     device `dev`; None stays None."""
     if t is None:
         return None
-    if not t.is_cuda or t.get_device() != dev:
-        raise ValueError(f"sp24: {name} must be a CUDA tensor on the current device ({dev})")
-    if t.dtype not in dtypes:
-        raise ValueError(f"sp24: {name} has type {t.dtype}, expected one of {dtypes}")
-    if t.numel() != numel or not t.is_contiguous():
+    if (t.get_device() != dev or t.dtype not in dtypes or t.numel() != numel
+            or not t.is_contiguous()):
+        if t.get_device() != dev:
+            raise ValueError(f"sp24: {name} must be a CUDA tensor on the current device ({dev})")
+        if t.dtype not in dtypes:
+            raise ValueError(f"sp24: {name} has type {t.dtype}, expected one of {tuple(dtypes)}")
         raise ValueError(f"sp24: {name} must be contiguous with {numel} elements")
     return t.data_ptr()
 
