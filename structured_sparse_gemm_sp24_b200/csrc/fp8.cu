@@ -34,7 +34,42 @@ struct ConvertArgs {
   int scale_cols;
 };
 
-template <bool kPrune, bool kWanda>
+// Magnitude selection of two groups of four at once: q.x, q.y hold the first
+// group (positions 0..3), q.z, q.w the second.  Position p of both groups is
+// put into the halves of one word as a 15-bit magnitude, so comparisons run two
+// at a time with the free top bit of each half as the guard: the top bit of
+// (x | 8000) - y says x >= y.  With a >= b the ordered positions 0, 1 and c >= d
+// the ordered 2, 3 (ties to the lower index), the two kept are
+//   0, 1 if b >= c;  2, 3 if d > a;  the larger of either pair otherwise.
+// Returns the two metadata nibbles lo | hi << 2 in one byte; `top` receives the
+// largest magnitude of either group (always kept).
+__device__ __forceinline__ uint32_t select2_mag(const uint4& q, uint32_t& top) {
+  constexpr uint32_t kG = 0x80008000u, kM = 0x7FFF7FFFu;
+  const uint32_t x = q.x & kM, y = q.y & kM, z = q.z & kM, w = q.w & kM;
+  const uint32_t p0 = __byte_perm(x, z, 0x5410), p1 = __byte_perm(x, z, 0x7632);
+  const uint32_t p2 = __byte_perm(y, w, 0x5410), p3 = __byte_perm(y, w, 0x7632);
+  const uint32_t a = __vmaxu2(p0, p1), b = __vminu2(p0, p1);
+  const uint32_t c = __vmaxu2(p2, p3), d = __vminu2(p2, p3);
+  const uint32_t ge01 = (p0 | kG) - p1;   // flags in bits 15 and 31
+  const uint32_t ge23 = (p2 | kG) - p3;
+  const uint32_t first = (b | kG) - c;    // keep 0, 1
+  const uint32_t not_last = (a | kG) - d; // clear: keep 2, 3
+  top = __vmaxu2(a, c);
+  const uint32_t lo0 = ~first & not_last & ~ge01, lo1 = ~not_last;
+  const uint32_t hi0 = first | ~not_last | ~ge23, hi1 = ~first;
+  const uint32_t t = ((lo0 >> 15) & 0x00010001u) | ((lo1 >> 14) & 0x00020002u) |
+                     ((hi0 >> 13) & 0x00040004u) | ((hi1 >> 12) & 0x00080008u);
+  return (t | (t >> 12)) & 0xFFu;
+}
+
+// Kept pair of a group (w0, w1 its four bf16) from its metadata nibble.
+__device__ __forceinline__ uint32_t gather_code(uint32_t w0, uint32_t w1, uint32_t code) {
+  return __byte_perm(w0, w1, 0x1010u + 0x22u * (code & 3u) + 0x880u * (code & 12u));
+}
+
+// kPrune: the mask is formed here (kWanda: scores |w| * norm; kMaskIn: positions
+// dropped by mask_in score 0), else mask_in is the mask.
+template <bool kPrune, bool kWanda, bool kMaskIn>
 __global__ void __launch_bounds__(kConvThreads) convert_fp8_kernel(const ConvertArgs a) {
   pdl_launch_dependents();
   pdl_wait_prior();
@@ -48,53 +83,56 @@ __global__ void __launch_bounds__(kConvThreads) convert_fp8_kernel(const Convert
   const int64_t kvec = a.k / 8;
   const int64_t v = static_cast<int64_t>(kb) * 16 + bb;
   const int64_t row0 = static_cast<int64_t>(rt) * 128 + m0;
-  const bool kv_ok = v < kvec;
+  // rows m0, m0 + 16, ... of the block that exist (for this thread's columns)
+  const int64_t left = v < kvec ? a.n - row0 : 0;
+  const int rows = left <= 0 ? 0 : (left >= 128 ? kConvRows : static_cast<int>((left + 15) / 16));
 
   uint4 q[kConvRows];
+  const uint4* src = reinterpret_cast<const uint4*>(a.w) + row0 * kvec + v;
 #pragma unroll
   for (int j = 0; j < kConvRows; ++j) {
-    const int64_t row = row0 + 16 * j;
     q[j] = make_uint4(0u, 0u, 0u, 0u);
-    if (kv_ok && row < a.n)
-      q[j] = __ldcs(reinterpret_cast<const uint4*>(a.w + row * a.k) + v);
+    if (j < rows) q[j] = __ldcs(src + 16 * j * kvec);
   }
   double nrm[8];
   if constexpr (kWanda) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) nrm[e] = kv_ok ? __ldg(a.norms + 8 * v + e) : 0.0;
+    for (int e = 0; e < 8; ++e) nrm[e] = rows > 0 ? __ldg(a.norms + 8 * v + e) : 0.0;
   }
 
   uint32_t bad = 0, amax = 0;
   uint32_t p0[kConvRows], p1[kConvRows];   // kept pairs of the two groups
 #pragma unroll
   for (int j = 0; j < kConvRows; ++j) {
-    const int64_t row = row0 + 16 * j;
-    uint32_t lo0 = 0, hi0 = 1, lo1 = 0, hi1 = 1, keep = 0;
-    if (kv_ok && row < a.n) {
-      uint32_t in = 0xFFu;
-      if (a.mask_in) in = a.mask_in[row * kvec + v];
-      if constexpr (kPrune && !kWanda) {
-        top2_positions_mag<true>(q[j].x, q[j].y, in & 15u, lo0, hi0);
-        top2_positions_mag<true>(q[j].z, q[j].w, in >> 4, lo1, hi1);
-        keep = (1u << lo0) | (1u << hi0) | (((1u << lo1) | (1u << hi1)) << 4);
-      } else {
-        if constexpr (kPrune) keep = mask_byte<true>(q[j], in, nrm, 2);
-        else keep = in;
-        uint32_t badv = 0;
-        const uint32_t c0 = nibble_code(keep & 15u, badv);
-        const uint32_t c1 = nibble_code(keep >> 4, badv);
-        if (!kPrune) bad |= badv;
-        lo0 = c0 & 3u; hi0 = c0 >> 2; lo1 = c1 & 3u; hi1 = c1 >> 2;
+    uint32_t code = 0x44u;                 // padding: positions (0, 1)
+    if constexpr (kPrune && !kWanda && !kMaskIn) {
+      uint32_t top;
+      code = select2_mag(q[j], top);       // (zeros keep 0, 1)
+      amax = __vmaxu2(amax, top);          // both halves hold magnitudes
+    } else {
+      uint32_t keep = 0x33u;
+      if (j < rows) {
+        uint32_t in = 0xFFu;
+        if (!kPrune || kMaskIn) in = a.mask_in[(row0 + 16 * j) * kvec + v];
+        if constexpr (!kPrune) keep = in;
+        else if constexpr (kWanda) keep = mask_byte<true>(q[j], in, nrm, 2);
+        else keep = keep_nibble_mag<true>(q[j].x, q[j].y, in & 15u, 2) |
+                    (keep_nibble_mag<true>(q[j].z, q[j].w, in >> 4, 2) << 4);
+        code = nibble_code(keep & 15u, bad) | (nibble_code(keep >> 4, bad) << 4);
       }
     }
-    p0[j] = gather_pair(q[j].x, q[j].y, lo0, hi0);
-    p1[j] = gather_pair(q[j].z, q[j].w, lo1, hi1);
-    s_meta[(m0 + 16 * j) * 16 + bb] = static_cast<uint8_t>(lo0 | (hi0 << 2) | (lo1 << 4) | (hi1 << 6));
-    s_mask[(m0 + 16 * j) * 16 + bb] = static_cast<uint8_t>(keep);
-    // |value| bits of a bf16 are its float's upper half
-    amax = max(amax, max((p0[j] << 16) & 0x7FFF0000u, p0[j] & 0x7FFF0000u));
-    amax = max(amax, max((p1[j] << 16) & 0x7FFF0000u, p1[j] & 0x7FFF0000u));
+    p0[j] = gather_code(q[j].x, q[j].y, code & 15u);
+    p1[j] = gather_code(q[j].z, q[j].w, code >> 4);
+    if constexpr (!(kPrune && !kWanda && !kMaskIn))
+      amax = __vmaxu2(amax, __vmaxu2(p0[j] & 0x7FFF7FFFu, p1[j] & 0x7FFF7FFFu));
+    s_meta[(m0 + 16 * j) * 16 + bb] = static_cast<uint8_t>(code);
+    if (a.mask_out)
+      s_mask[(m0 + 16 * j) * 16 + bb] = static_cast<uint8_t>(
+          (1u << (code & 3u)) | (1u << ((code >> 2) & 3u)) | (16u << ((code >> 4) & 3u)) |
+          (16u << (code >> 6)));
   }
+  // a bf16's bits are the upper half of its float's
+  amax = max(amax & 0xFFFFu, amax >> 16) << 16;
   amax = __reduce_max_sync(0xFFFFFFFFu, amax);
   if ((tid & 31) == 0) s_max[tid >> 5] = amax;
   __syncthreads();
@@ -102,36 +140,36 @@ __global__ void __launch_bounds__(kConvThreads) convert_fp8_kernel(const Convert
   for (int i = 0; i < kConvThreads / 32; ++i) amax = max(amax, s_max[i]);
   const uint32_t byte = scale_byte(amax);
   const float inv = scale_inverse(byte == kScaleNan ? kScaleOne : byte);
+  uint32_t* dst = a.vals + row0 * kvec + v;
 #pragma unroll
   for (int j = 0; j < kConvRows; ++j) {
-    const int64_t row = row0 + 16 * j;
-    if (kv_ok && row < a.n) {
+    if (j < rows) {
       uint32_t c = e4m3x4(__uint_as_float(p0[j] << 16) * inv,
                           __uint_as_float(p0[j] & 0xFFFF0000u) * inv,
                           __uint_as_float(p1[j] << 16) * inv,
                           __uint_as_float(p1[j] & 0xFFFF0000u) * inv);
       if (byte == kScaleNan) c = kCodeNan4;
-      __stcs(a.vals + row * kvec + v, c);
+      __stcs(dst + 16 * j * kvec, c);
     }
   }
   if (tid < 128) {
-    uint4* dst = reinterpret_cast<uint4*>(a.meta + static_cast<int64_t>(blockIdx.x) * 2048);
-    __stcs(dst + tid, reinterpret_cast<const uint4*>(s_meta)[tid]);
+    uint4* md = reinterpret_cast<uint4*>(a.meta + static_cast<int64_t>(blockIdx.x) * 2048);
+    __stcs(md + tid, reinterpret_cast<const uint4*>(s_meta)[tid]);
   } else if (a.mask_out) {
     const int m = tid - 128;
     const int64_t row = static_cast<int64_t>(rt) * 128 + m;
     const int64_t v0 = static_cast<int64_t>(kb) * 16;
     const int nb = static_cast<int>(kvec - v0 < 16 ? kvec - v0 : 16);   // K % 32: multiple of 4
     if (row < a.n) {
-      uint32_t* dst = reinterpret_cast<uint32_t*>(a.mask_out + row * kvec + v0);
-      for (int e = 0; e < nb / 4; ++e) dst[e] = reinterpret_cast<const uint32_t*>(s_mask)[m * 4 + e];
+      uint32_t* mo = reinterpret_cast<uint32_t*>(a.mask_out + row * kvec + v0);
+      for (int e = 0; e < nb / 4; ++e) mo[e] = reinterpret_cast<const uint32_t*>(s_mask)[m * 4 + e];
     }
   }
   // this block's scale, and the row's padding after the last block
   if (tid == 0) a.e_w[static_cast<int64_t>(rt) * a.scale_cols + kb] = static_cast<uint8_t>(byte);
   if (kb == a.kblocks - 1 && tid > 0 && kb + tid < a.scale_cols)
     a.e_w[static_cast<int64_t>(rt) * a.scale_cols + kb + tid] = static_cast<uint8_t>(kScaleOne);
-  if (bad) raise_error(kErrPatternBit);
+  if (!kPrune && bad) raise_error(kErrPatternBit);
 }
 
 static sp24_status launch_convert_fp8(bool prune, bool wanda, ConvertArgs a, cudaStream_t s) {
@@ -141,9 +179,13 @@ static sp24_status launch_convert_fp8(bool prune, bool wanda, ConvertArgs a, cud
   a.kblocks = static_cast<int>(kblocks);
   a.scale_cols = static_cast<int>(4 * ((a.k + 511) / 512));
   const dim3 grid(static_cast<unsigned>(nblocks));
-  if (!prune) return launch_kernel(convert_fp8_kernel<false, false>, grid, dim3(kConvThreads), 0, s, 1, a);
-  if (wanda) return launch_kernel(convert_fp8_kernel<true, true>, grid, dim3(kConvThreads), 0, s, 1, a);
-  return launch_kernel(convert_fp8_kernel<true, false>, grid, dim3(kConvThreads), 0, s, 1, a);
+  const dim3 block(kConvThreads);
+  if (!prune) return launch_kernel(convert_fp8_kernel<false, false, true>, grid, block, 0, s, 1, a);
+  if (wanda)
+    return a.mask_in ? launch_kernel(convert_fp8_kernel<true, true, true>, grid, block, 0, s, 1, a)
+                     : launch_kernel(convert_fp8_kernel<true, true, false>, grid, block, 0, s, 1, a);
+  return a.mask_in ? launch_kernel(convert_fp8_kernel<true, false, true>, grid, block, 0, s, 1, a)
+                   : launch_kernel(convert_fp8_kernel<true, false, false>, grid, block, 0, s, 1, a);
 }
 
 }  // namespace sp24

@@ -115,11 +115,9 @@ struct NormArgs {
   int64_t m, k;
   float eps;
   int scale_cols;
-  int segs;             // column segments of a row (quantisation only, else 1)
-  int seg_len;          // columns per segment, a multiple of 512
 };
 
-template <typename T, int OUT, bool kNorm, int NV, bool kWarpRow>
+template <typename T, int OUT, int NV, bool kWarpRow>
 __global__ void __launch_bounds__(kWarpRow ? 256 : 1024)
 norm_kernel(const NormArgs a) {
   pdl_launch_dependents();
@@ -128,11 +126,11 @@ norm_kernel(const NormArgs a) {
   const int lane = threadIdx.x & 31;
   const int t = kWarpRow ? lane : static_cast<int>(threadIdx.x);
   const int nt = kWarpRow ? 32 : static_cast<int>(blockDim.x);
-  const int64_t rows = a.m * a.segs;
   const int per_cta = kWarpRow ? static_cast<int>(blockDim.x >> 5) : 1;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * per_cta + (kWarpRow ? threadIdx.x >> 5 : 0);
   const int64_t step = static_cast<int64_t>(gridDim.x) * per_cta;
-  const bool res = kNorm && a.r != nullptr;
+  const bool res = a.r != nullptr;
+  const int c_end = static_cast<int>(a.k / 8);
   const T* gamma = static_cast<const T*>(a.gamma);
   float sx = 1.0f, rsx = 1.0f;
   if constexpr (OUT == SP24_INT8) {
@@ -141,13 +139,9 @@ norm_kernel(const NormArgs a) {
   }
 
   Vec8<T> x[NV], r[NV];
-  auto load = [&](int64_t vr) {
-    const int64_t row = kNorm ? vr : vr / a.segs;
-    const int col0 = kNorm ? 0 : static_cast<int>(vr - row * a.segs) * a.seg_len;
-    const int64_t left = a.k - col0;
-    const int c_end = static_cast<int>((kNorm || left < a.seg_len ? left : a.seg_len) / 8);
-    const T* xp = static_cast<const T*>(a.x) + row * a.k + col0;
-    const T* rp = static_cast<const T*>(a.r) + row * a.k + col0;
+  auto load = [&](int64_t row) {
+    const T* xp = static_cast<const T*>(a.x) + row * a.k;
+    const T* rp = static_cast<const T*>(a.r) + row * a.k;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = t + i * nt;
@@ -160,15 +154,10 @@ norm_kernel(const NormArgs a) {
       }
     }
   };
-  if (first < rows) load(first);
+  if (first < a.m) load(first);
   uint32_t buf = 0;
-  for (int64_t vr = first; vr < rows; vr += step, buf ^= 1u) {
-    const int64_t row = kNorm ? vr : vr / a.segs;
-    const int seg = kNorm ? 0 : static_cast<int>(vr - row * a.segs);
-    const int col0 = seg * a.seg_len;
-    const int64_t left = a.k - col0;
-    const int c_end = static_cast<int>((kNorm || left < a.seg_len ? left : a.seg_len) / 8);
-    const int64_t base = row * a.k + col0;
+  for (int64_t row = first; row < a.m; row += step, buf ^= 1u) {
+    const int64_t base = row * a.k;
     Vec8<T> h[NV];
     float sum = 0.0f;
 #pragma unroll
@@ -184,36 +173,29 @@ norm_kernel(const NormArgs a) {
       } else {
         h[i] = x[i];
       }
-      if constexpr (kNorm) {
-        float f[8];
-        h[i].get(f);   // the norm is that of the stored sum
+      float f[8];
+      h[i].get(f);   // the norm is that of the stored sum
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum = __fmaf_rn(f[j], f[j], sum);
-        if (a.h != nullptr && c < c_end) h[i].store(static_cast<T*>(a.h) + base + 8 * c);
-      }
+      for (int j = 0; j < 8; ++j) sum = __fmaf_rn(f[j], f[j], sum);
+      if (a.h != nullptr && c < c_end) h[i].store(static_cast<T*>(a.h) + base + 8 * c);
     }
-    if (vr + step < rows) load(vr + step);
-    float rs = 1.0f;
-    if constexpr (kNorm) {
-      sum = row_sum<kWarpRow>(sum, part, buf);
-      rs = __frsqrt_rn(__fadd_rn(__fdiv_rn(sum, static_cast<float>(a.k)), a.eps));
-      if (a.rstd != nullptr && t == 0) a.rstd[row] = rs;
-    }
+    if (row + step < a.m) load(row + step);
+    sum = row_sum<kWarpRow>(sum, part, buf);
+    const float rs = __frsqrt_rn(__fadd_rn(__fdiv_rn(sum, static_cast<float>(a.k)), a.eps));
+    if (a.rstd != nullptr && t == 0) a.rstd[row] = rs;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = t + i * nt;
       const bool ok = c < c_end;
       float f[8];
       h[i].get(f);
-      if constexpr (kNorm) {
-        Vec8<T> g;
-        g.zero();
-        if (ok) g.load_cached(gamma + 8 * c);
-        float fg[8];
-        g.get(fg);
+      Vec8<T> g;
+      g.zero();
+      if (ok) g.load_cached(gamma + 8 * c);
+      float fg[8];
+      g.get(fg);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = __fmul_rn(__fmul_rn(f[j], rs), fg[j]);
-      }
+      for (int j = 0; j < 8; ++j) f[j] = __fmul_rn(__fmul_rn(f[j], rs), fg[j]);
       if constexpr (OUT == SP24_FP8) {
         uint32_t amax = 0;
 #pragma unroll
@@ -230,7 +212,7 @@ norm_kernel(const NormArgs a) {
           if (byte == kScaleNan) q.x = q.y = kCodeNan4;
           *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.y) + base + 8 * c) = q;
           if ((lane & 15) == 0)
-            a.e[row * a.scale_cols + (col0 >> 7) + (c >> 4)] = static_cast<uint8_t>(byte);
+            a.e[row * a.scale_cols + (c >> 4)] = static_cast<uint8_t>(byte);
         }
       } else if constexpr (OUT == SP24_INT8) {
         if (ok) {
@@ -251,8 +233,78 @@ norm_kernel(const NormArgs a) {
     }
     if constexpr (OUT == SP24_FP8) {   // the scale row's padding
       const int kb = static_cast<int>((a.k + 127) >> 7);
-      if (seg == a.segs - 1 && t < a.scale_cols - kb)
+      if (t < a.scale_cols - kb)
         a.e[row * a.scale_cols + kb + t] = static_cast<uint8_t>(kScaleOne);
+    }
+  }
+}
+
+// ------------------------------------------------------------ quantisation
+// e4m3 codes of [m][k] by blocks of 128 columns.  A half-warp takes a block and
+// a thread kQuantUnroll of its vectors of 8 columns, all loaded before the first
+// is used; blocks are numbered through the rows, so consecutive half-warps read
+// consecutive memory whatever the row length.
+constexpr int kQuantUnroll = 4;
+constexpr int kQuantThreads = 256;
+
+struct QuantArgs {
+  const void* x;
+  uint8_t* y;
+  uint8_t* e;
+  int64_t k;
+  uint32_t blocks;      // m * kb
+  uint32_t kb;          // blocks of a row
+  int scale_cols;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kQuantThreads) quantize_fp8_kernel(const QuantArgs a) {
+  pdl_launch_dependents();
+  pdl_wait_prior();
+  constexpr uint32_t kHalves = kQuantThreads / 16;
+  const uint32_t hw = threadIdx.x >> 4, t = threadIdx.x & 15;
+  // 32-bit block numbers: m * kb < 2^31, checked by the host
+  const uint32_t step = gridDim.x * (kHalves * kQuantUnroll);
+  for (uint32_t b0 = blockIdx.x * (kHalves * kQuantUnroll); b0 < a.blocks; b0 += step) {
+    Vec8<T> x[kQuantUnroll];
+    uint32_t row[kQuantUnroll], col[kQuantUnroll];
+    bool ok[kQuantUnroll];
+#pragma unroll
+    for (int u = 0; u < kQuantUnroll; ++u) {
+      const uint32_t b = b0 + u * kHalves + hw;
+      row[u] = b / a.kb;
+      col[u] = b - row[u] * a.kb;
+      const int64_t c = static_cast<int64_t>(col[u]) * 128 + 8 * t;
+      ok[u] = b < a.blocks && c < a.k;
+      x[u].zero();
+      if (ok[u]) x[u].load(static_cast<const T*>(a.x) + row[u] * a.k + c);
+    }
+#pragma unroll
+    for (int u = 0; u < kQuantUnroll; ++u) {
+      float f[8];
+      x[u].get(f);
+      uint32_t amax = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) amax = max(amax, abs_bits(f[j]));
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+      const uint32_t byte = scale_byte(amax);
+      const float inv = scale_inverse(byte == kScaleNan ? kScaleOne : byte);
+      if (ok[u]) {
+        uint2 q;
+        q.x = e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
+        q.y = e4m3x4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv);
+        if (byte == kScaleNan) q.x = q.y = kCodeNan4;
+        *reinterpret_cast<uint2*>(a.y + row[u] * a.k + static_cast<int64_t>(col[u]) * 128 + 8 * t) = q;
+        // the scale, and after a row's last block the row's padding
+        uint8_t* e = a.e + static_cast<int64_t>(row[u]) * a.scale_cols + col[u];
+        if (t == 0) {
+          e[0] = static_cast<uint8_t>(byte);
+          if (col[u] == a.kb - 1)
+            for (int i = 1; i < a.scale_cols - static_cast<int>(col[u]); ++i)
+              e[i] = static_cast<uint8_t>(kScaleOne);
+        }
+      }
     }
   }
 }
@@ -458,14 +510,14 @@ static sp24_status resident_blocks(const void* kern, Occupancy& o, int threads, 
   return SP24_OK;
 }
 
-template <typename T, int OUT, bool kNorm, int NV, bool kWarpRow>
+template <typename T, int OUT, int NV, bool kWarpRow>
 static sp24_status launch_norm_t(const NormArgs& a, int threads, cudaStream_t s) {
-  auto kern = norm_kernel<T, OUT, kNorm, NV, kWarpRow>;
+  auto kern = norm_kernel<T, OUT, NV, kWarpRow>;
   static Occupancy occ;
   int per_sm = 0;
   SP24_TRY(resident_blocks(reinterpret_cast<const void*>(kern), occ, threads, 0, &per_sm));
   const int64_t per_cta = kWarpRow ? threads / 32 : 1;
-  const int64_t ctas = (a.m * a.segs + per_cta - 1) / per_cta;
+  const int64_t ctas = (a.m + per_cta - 1) / per_cta;
   const int64_t cap = static_cast<int64_t>(sm_count()) * per_sm;
   return launch_kernel(kern, dim3(static_cast<unsigned>(ctas < cap ? ctas : cap)), dim3(threads), 0,
                        s, 1, a);
@@ -473,36 +525,37 @@ static sp24_status launch_norm_t(const NormArgs& a, int threads, cudaStream_t s)
 
 static int round32(int64_t v) { return static_cast<int>((v + 31) / 32 * 32); }
 
-template <typename T, int OUT, bool kNorm>
+template <typename T, int OUT>
 static sp24_status launch_norm(const NormArgs& a, cudaStream_t s) {
-  const int64_t c = (kNorm || a.k < a.seg_len ? a.k : a.seg_len) / 8;   // vectors of a row
-  if (c <= 32) return launch_norm_t<T, OUT, kNorm, 1, true>(a, 256, s);
-  if (c <= 64) return launch_norm_t<T, OUT, kNorm, 2, true>(a, 256, s);
-  if (c <= 128) return launch_norm_t<T, OUT, kNorm, 4, true>(a, 256, s);
-  if (c <= 1024 && a.m * a.segs <= 2 * sm_count())
-    return launch_norm_t<T, OUT, kNorm, 1, false>(a, round32(c), s);
-  return launch_norm_t<T, OUT, kNorm, 2, false>(a, round32((c + 1) / 2), s);
+  const int64_t c = a.k / 8;   // vectors of a row
+  if (c <= 32) return launch_norm_t<T, OUT, 1, true>(a, 256, s);
+  if (c <= 64) return launch_norm_t<T, OUT, 2, true>(a, 256, s);
+  if (c <= 128) return launch_norm_t<T, OUT, 4, true>(a, 256, s);
+  if (c <= 1024 && a.m <= 2 * sm_count())
+    return launch_norm_t<T, OUT, 1, false>(a, round32(c), s);
+  return launch_norm_t<T, OUT, 2, false>(a, round32((c + 1) / 2), s);
 }
 
-template <bool kNorm>
-static sp24_status launch_norm_out(const NormArgs& a, int x_dtype, int out, cudaStream_t s) {
-  if constexpr (!kNorm) {
-    return x_dtype == SP24_F32 ? launch_norm<float, SP24_FP8, false>(a, s)
-                               : launch_norm<__nv_bfloat16, SP24_FP8, false>(a, s);
-  } else {
-    const bool f32 = x_dtype == SP24_F32;
-    switch (out) {
-      case SP24_FP8:
-        return f32 ? launch_norm<float, SP24_FP8, true>(a, s)
-                   : launch_norm<__nv_bfloat16, SP24_FP8, true>(a, s);
-      case SP24_INT8:
-        return f32 ? launch_norm<float, SP24_INT8, true>(a, s)
-                   : launch_norm<__nv_bfloat16, SP24_INT8, true>(a, s);
-      default:
-        return f32 ? launch_norm<float, SP24_BF16, true>(a, s)
-                   : launch_norm<__nv_bfloat16, SP24_BF16, true>(a, s);
-    }
+template <typename T>
+static sp24_status launch_norm_out(const NormArgs& a, int out, cudaStream_t s) {
+  switch (out) {
+    case SP24_FP8: return launch_norm<T, SP24_FP8>(a, s);
+    case SP24_INT8: return launch_norm<T, SP24_INT8>(a, s);
+    default: return launch_norm<T, SP24_BF16>(a, s);
   }
+}
+
+template <typename T>
+static sp24_status launch_quantize(const QuantArgs& a, cudaStream_t s) {
+  auto kern = quantize_fp8_kernel<T>;
+  static Occupancy occ;
+  int per_sm = 0;
+  SP24_TRY(resident_blocks(reinterpret_cast<const void*>(kern), occ, kQuantThreads, 0, &per_sm));
+  const int64_t per_cta = kQuantThreads / 16 * kQuantUnroll;
+  const int64_t ctas = (static_cast<int64_t>(a.blocks) + per_cta - 1) / per_cta;
+  const int64_t cap = static_cast<int64_t>(sm_count()) * per_sm;
+  return launch_kernel(kern, dim3(static_cast<unsigned>(ctas < cap ? ctas : cap)),
+                       dim3(kQuantThreads), 0, s, 1, a);
 }
 
 // Rows of the dgamma workspace: at most this many blocks run the backward.
@@ -570,9 +623,8 @@ sp24_status sp24_rmsnorm_quant(const void* X, const void* R, const void* gamma, 
   a.k = K;
   a.eps = eps;
   a.scale_cols = static_cast<int>(4 * ((K + 511) / 512));
-  a.segs = 1;
-  a.seg_len = 0;
-  return launch_norm_out<true>(a, x_dtype, out_dtype, as_stream(stream));
+  return x_dtype == SP24_F32 ? launch_norm_out<float>(a, out_dtype, as_stream(stream))
+                             : launch_norm_out<__nv_bfloat16>(a, out_dtype, as_stream(stream));
 }
 
 sp24_status sp24_quantize_fp8(const void* X, int64_t M, int64_t K, int x_dtype, void* Xq,
@@ -582,18 +634,19 @@ sp24_status sp24_quantize_fp8(const void* X, int64_t M, int64_t K, int x_dtype, 
   if (M == 0) return SP24_OK;
   if (!X || !Xq || !e_x) return SP24_ERR_ARG;
   if (!aligned16(X) || !aligned16(Xq) || !aligned16(e_x)) return SP24_ERR_ALIGN;
-  if (K > 0x7FFFFFFF - 4096) return SP24_ERR_UNSUPPORTED;
+  const int64_t kb = K / 128 + (K % 128 != 0);
+  if (kb > 0x7FFFFFFF / M) return SP24_ERR_UNSUPPORTED;   // more blocks than 32 bits number
   SP24_TRY(check_device());
-  NormArgs a{};
+  QuantArgs a{};
   a.x = X;
-  a.y = Xq;
+  a.y = static_cast<uint8_t*>(Xq);
   a.e = e_x;
-  a.m = M;
   a.k = K;
+  a.blocks = static_cast<uint32_t>(M * kb);
+  a.kb = static_cast<uint32_t>(kb);
   a.scale_cols = static_cast<int>(4 * ((K + 511) / 512));
-  a.seg_len = 4096;
-  a.segs = static_cast<int>((K + a.seg_len - 1) / a.seg_len);
-  return launch_norm_out<false>(a, x_dtype, SP24_FP8, as_stream(stream));
+  return x_dtype == SP24_F32 ? launch_quantize<float>(a, as_stream(stream))
+                             : launch_quantize<__nv_bfloat16>(a, as_stream(stream));
 }
 
 size_t sp24_rmsnorm_backward_workspace_bytes(int64_t M, int64_t K) {
