@@ -13,7 +13,7 @@
 // once; a row lives in registers between its sum and its output.  A thread
 // holds NV vectors of 8 columns (16 bytes of bf16), T threads apart, so 16
 // neighbouring lanes hold a 128-column block and its maximum is four shuffles.
-// Rows of up to 1024 columns take one warp (no barrier); longer rows a block
+// Rows of up to 512 columns take one warp (no barrier); longer rows a block
 // of T threads and one barrier.  The grid is persistent, and a row's loads are
 // issued before the previous row is reduced and written.
 
@@ -51,6 +51,18 @@ struct Vec8<__nv_bfloat16> {
       f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
     }
   }
+  // += v, each sum rounded once (the bf16 adder rounds the exact sum)
+  __device__ __forceinline__ void add(const Vec8& v) {
+    q.x = add2(q.x, v.q.x);
+    q.y = add2(q.y, v.q.y);
+    q.z = add2(q.z, v.q.z);
+    q.w = add2(q.w, v.q.w);
+  }
+  __device__ __forceinline__ static uint32_t add2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+  }
   __device__ __forceinline__ void set(const float (&f)[8]) {   // round to nearest even
     q = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
                    pack_bf16x2(f[6], f[7]));
@@ -78,6 +90,14 @@ struct Vec8<float> {
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
   }
+  __device__ __forceinline__ void add(const Vec8& v) {
+    float f[8], g[8];
+    get(f);
+    v.get(g);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = __fadd_rn(f[i], g[i]);
+    set(f);
+  }
   __device__ __forceinline__ void set(const float (&f)[8]) {
     a = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
                    __float_as_uint(f[3]));
@@ -86,19 +106,36 @@ struct Vec8<float> {
   }
 };
 
-// Sum over the threads of a row, the same value in all of them: the warp's by
-// shuffles, then (kWarpRow = false) the warps' in warp order through `part`,
-// which alternates between two rows' buffers so that one barrier is enough.
+// Largest magnitude of eight values as float bits; a NaN among them gives a NaN.
+__device__ __forceinline__ uint32_t amax8(const float (&f)[8]) {
+  float a, b, c;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(a) : "f"(f[0]), "f"(f[1]), "f"(f[2]));
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(b) : "f"(f[3]), "f"(f[4]), "f"(f[5]));
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(c) : "f"(f[6]), "f"(f[7]), "f"(a));
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(a) : "f"(b), "f"(c), "f"(c));
+  return __float_as_uint(a);
+}
+
+// Largest value of the 16 lanes that hold a block.
+__device__ __forceinline__ uint32_t block_max(uint32_t v) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+  return v;
+}
+
+// Sum over the `warps` warps of a row, the same value in all threads: each
+// warp's by shuffles, then the warps' in order through `part`, of which two
+// rows' buffers alternate so that one barrier (hardware barrier `bar`, of the
+// row's threads) is enough.
 template <bool kWarpRow>
-__device__ __forceinline__ float row_sum(float v, float (&part)[2][32], uint32_t buf) {
+__device__ __forceinline__ float row_sum(float v, float* part, int warp, int warps, uint32_t bar) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   if constexpr (kWarpRow) return v;
-  const int warps = blockDim.x >> 5;
-  if ((threadIdx.x & 31) == 0) part[buf][threadIdx.x >> 5] = v;
-  __syncthreads();
+  if ((threadIdx.x & 31) == 0) part[warp] = v;
+  named_barrier(bar, 32 * warps);
   float t = 0.0f;
-  for (int i = 0; i < warps; ++i) t += part[buf][i];
+  for (int i = 0; i < warps; ++i) t += part[i];
   return t;
 }
 
@@ -117,25 +154,91 @@ struct NormArgs {
   int scale_cols;
 };
 
+// h of one vector: x + r rounded to the stream's type (x without r), and its
+// squares added to `sum` in fp32.  The norm is that of the stored sum.
+template <typename T>
+__device__ __forceinline__ Vec8<T> norm_sum(const Vec8<T>& x, const Vec8<T>& r, bool res, float& sum) {
+  Vec8<T> h = x;
+  if (res) h.add(r);
+  float f[8];
+  h.get(f);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sum = __fmaf_rn(f[j], f[j], sum);
+  return h;
+}
+
+// y of one vector (columns 8c ..) of row `row` and its output.  All lanes of a
+// warp call it, `ok` where the columns exist: 16 neighbouring lanes hold a
+// 128-column block.
+template <typename T, int OUT>
+__device__ __forceinline__ void norm_out(const NormArgs& a, const Vec8<T>& h, const Vec8<T>& g,
+                                         float rs, int64_t row, int c, bool ok, float sx, float rsx) {
+  float f[8], fg[8];
+  h.get(f);
+  g.get(fg);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f[j] = __fmul_rn(__fmul_rn(f[j], rs), fg[j]);
+  const int64_t at = row * a.k + 8 * c;
+  if constexpr (OUT == SP24_FP8) {
+    // (a NaN statistic makes NaNs of the zeros past the row)
+    const uint32_t amax = block_max(ok ? amax8(f) : 0u);
+    const uint32_t byte = scale_byte(amax);
+    const float inv = scale_inverse(byte == kScaleNan ? kScaleOne : byte);
+    if (ok) {
+      uint2 q;
+      q.x = e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
+      q.y = e4m3x4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv);
+      if (byte == kScaleNan) q.x = q.y = kCodeNan4;
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.y) + at) = q;
+      if ((threadIdx.x & 15) == 0) a.e[row * a.scale_cols + (c >> 4)] = static_cast<uint8_t>(byte);
+    }
+  } else if constexpr (OUT == SP24_INT8) {
+    if (ok) {
+      uint2 q;
+      q.x = q8(f[0], sx, rsx) | (q8(f[1], sx, rsx) << 8) | (q8(f[2], sx, rsx) << 16) |
+            (q8(f[3], sx, rsx) << 24);
+      q.y = q8(f[4], sx, rsx) | (q8(f[5], sx, rsx) << 8) | (q8(f[6], sx, rsx) << 16) |
+            (q8(f[7], sx, rsx) << 24);
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.y) + at) = q;
+    }
+  } else {
+    if (ok) {
+      Vec8<__nv_bfloat16> o;
+      o.set(f);
+      o.store(static_cast<__nv_bfloat16*>(a.y) + at);
+    }
+  }
+}
+
+__device__ __forceinline__ float norm_rstd(float sum, const NormArgs& a) {
+  return __frsqrt_rn(__fadd_rn(__fdiv_rn(sum, static_cast<float>(a.k)), a.eps));
+}
+
+// Per row: 1 / rms, and (e4m3) the padding of the scale row, by thread t of the row.
+template <int OUT>
+__device__ __forceinline__ void norm_row_end(const NormArgs& a, int64_t row, int t, float rs) {
+  if (a.rstd != nullptr && t == 0) a.rstd[row] = rs;
+  if constexpr (OUT == SP24_FP8) {
+    const int kb = static_cast<int>((a.k + 127) >> 7);
+    if (t < a.scale_cols - kb) a.e[row * a.scale_cols + kb + t] = static_cast<uint8_t>(kScaleOne);
+  }
+}
+
+// Rows straight from global memory: short rows (one warp each) and few rows.
 template <typename T, int OUT, int NV, bool kWarpRow, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) norm_kernel(const NormArgs a) {
   pdl_launch_dependents();
   pdl_wait_prior();
   __shared__ float part[2][32];
-  const int lane = threadIdx.x & 31;
-  const int t = kWarpRow ? lane : static_cast<int>(threadIdx.x);
+  const int t = kWarpRow ? static_cast<int>(threadIdx.x & 31) : static_cast<int>(threadIdx.x);
   const int nt = kWarpRow ? 32 : static_cast<int>(blockDim.x);
   const int per_cta = kWarpRow ? static_cast<int>(blockDim.x >> 5) : 1;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * per_cta + (kWarpRow ? threadIdx.x >> 5 : 0);
   const int64_t step = static_cast<int64_t>(gridDim.x) * per_cta;
   const bool res = a.r != nullptr;
   const int c_end = static_cast<int>(a.k / 8);
-  const T* gamma = static_cast<const T*>(a.gamma);
-  float sx = 1.0f, rsx = 1.0f;
-  if constexpr (OUT == SP24_INT8) {
-    sx = *a.s_x;
-    rsx = __frcp_rn(sx);
-  }
+  const float sx = OUT == SP24_INT8 ? *a.s_x : 1.0f;
+  const float rsx = __frcp_rn(sx);
 
   Vec8<T> x[NV], r[NV];
   auto load = [&](int64_t row) {
@@ -144,100 +247,39 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_kernel(const NormArgs a) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = t + i * nt;
+      x[i].zero();
+      if (res) r[i].zero();
       if (c < c_end) {
         x[i].load(xp + 8 * c);
         if (res) r[i].load(rp + 8 * c);
-      } else {
-        x[i].zero();
-        if (res) r[i].zero();
       }
     }
   };
-  // the next row's loads are issued before this one is reduced, where the
-  // registers allow (two rows of float32 would halve the resident threads)
-  constexpr bool kAhead = sizeof(T) == 2;
+  // the next row is loaded before this one is reduced, where the registers
+  // allow (two float32 rows of two vectors would spill)
+  constexpr bool kAhead = sizeof(T) * NV <= 4 || kWarpRow;
   if (kAhead && first < a.m) load(first);
   uint32_t buf = 0;
   for (int64_t row = first; row < a.m; row += step, buf ^= 1u) {
-    const int64_t base = row * a.k;
     if (!kAhead) load(row);
     Vec8<T> h[NV];
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = t + i * nt;
-      if (res) {
-        float fx[8], fr[8];
-        x[i].get(fx);
-        r[i].get(fr);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) fx[j] += fr[j];
-        h[i].set(fx);
-      } else {
-        h[i] = x[i];
-      }
-      float f[8];
-      h[i].get(f);   // the norm is that of the stored sum
-#pragma unroll
-      for (int j = 0; j < 8; ++j) sum = __fmaf_rn(f[j], f[j], sum);
-      if (a.h != nullptr && c < c_end) h[i].store(static_cast<T*>(a.h) + base + 8 * c);
+      h[i] = norm_sum<T>(x[i], r[i], res, sum);
+      if (a.h != nullptr && c < c_end) h[i].store(static_cast<T*>(a.h) + row * a.k + 8 * c);
     }
     if (kAhead && row + step < a.m) load(row + step);
-    sum = row_sum<kWarpRow>(sum, part, buf);
-    const float rs = __frsqrt_rn(__fadd_rn(__fdiv_rn(sum, static_cast<float>(a.k)), a.eps));
-    if (a.rstd != nullptr && t == 0) a.rstd[row] = rs;
+    const float rs = norm_rstd(row_sum<kWarpRow>(sum, part[buf], threadIdx.x >> 5, blockDim.x >> 5, 0), a);
+    norm_row_end<OUT>(a, row, t, rs);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = t + i * nt;
-      const bool ok = c < c_end;
-      float f[8];
-      h[i].get(f);
       Vec8<T> g;
       g.zero();
-      if (ok) g.load_cached(gamma + 8 * c);
-      float fg[8];
-      g.get(fg);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = __fmul_rn(__fmul_rn(f[j], rs), fg[j]);
-      if constexpr (OUT == SP24_FP8) {
-        uint32_t amax = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) amax = max(amax, abs_bits(f[j]));
-        if (!ok) amax = 0;   // (a NaN statistic makes NaNs of the zeros past the row)
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-        const uint32_t byte = scale_byte(amax);
-        const float inv = scale_inverse(byte == kScaleNan ? kScaleOne : byte);
-        if (ok) {
-          uint2 q;
-          q.x = e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
-          q.y = e4m3x4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv);
-          if (byte == kScaleNan) q.x = q.y = kCodeNan4;
-          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.y) + base + 8 * c) = q;
-          if ((lane & 15) == 0)
-            a.e[row * a.scale_cols + (c >> 4)] = static_cast<uint8_t>(byte);
-        }
-      } else if constexpr (OUT == SP24_INT8) {
-        if (ok) {
-          uint2 q;
-          q.x = q8(f[0], sx, rsx) | (q8(f[1], sx, rsx) << 8) | (q8(f[2], sx, rsx) << 16) |
-                (q8(f[3], sx, rsx) << 24);
-          q.y = q8(f[4], sx, rsx) | (q8(f[5], sx, rsx) << 8) | (q8(f[6], sx, rsx) << 16) |
-                (q8(f[7], sx, rsx) << 24);
-          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.y) + base + 8 * c) = q;
-        }
-      } else {
-        if (ok) {
-          Vec8<__nv_bfloat16> o;
-          o.set(f);
-          o.store(static_cast<__nv_bfloat16*>(a.y) + base + 8 * c);
-        }
-      }
-    }
-    if constexpr (OUT == SP24_FP8) {   // the scale row's padding
-      const int kb = static_cast<int>((a.k + 127) >> 7);
-      if (t < a.scale_cols - kb)
-        a.e[row * a.scale_cols + kb + t] = static_cast<uint8_t>(kScaleOne);
+      if (c < c_end) g.load_cached(static_cast<const T*>(a.gamma) + 8 * c);
+      norm_out<T, OUT>(a, h[i], g, rs, row, c, c < c_end, sx, rsx);
     }
   }
 }
@@ -311,9 +353,7 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_fp8_kernel(const Quant
   }
 #pragma unroll
   for (int u = 0; u < kQuantUnroll; ++u) {
-    uint32_t amax = amax8(x[u]);
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+    const uint32_t amax = block_max(amax8(x[u]));
     const uint32_t byte = scale_byte(amax);
     const float inv = scale_inverse(byte == kScaleNan ? kScaleOne : byte);
     if (at[u] >= 0) {
@@ -336,11 +376,17 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_fp8_kernel(const Quant
 }
 
 // ----------------------------------------------------------------- backward
-// With g = dy * gamma and xh = h * rstd:
-//   dx = rstd * (g - xh * mean(g * xh)) [+ dh],   dgamma = sum over rows dy * xh.
-// A thread keeps the dgamma sums of its columns over all rows of its block and
-// writes them once, to a row of the workspace; dgamma_kernel adds the rows in
-// order (no atomics: the same inputs give the same bits).
+// With t = dy * h:  dgamma = sum over rows of t * rstd, and
+//   dx = rstd * dy * gamma - h * c [+ dh],  c = rstd^3 * mean(t * gamma),
+// which is rstd * (g - xh * mean(g * xh)) with g = dy * gamma, xh = h * rstd.
+// Bound by HBM: dy, h (and dh) are read once and dx is written once.
+//
+// A block holds groups of T threads, a row each at a time; a thread keeps the
+// dgamma sums of its columns over all its rows.  At the end the groups' sums are
+// added in order through shared memory and the block writes one row of the
+// workspace; dgamma_kernel adds those rows in order (no atomics: the same
+// inputs give the same bits).  Groups keep the workspace short (509 x 768: 5.1
+// us with eight rows a block, 9.9 us with one).
 struct BackArgs {
   const void* dy;
   const void* dh;       // optional
@@ -352,19 +398,18 @@ struct BackArgs {
   int64_t m, k;
 };
 
-template <typename T, int NV, bool kWarpRow>
-__global__ void __launch_bounds__(kWarpRow ? 256 : (NV == 1 ? 1024 : 512))
-norm_back_kernel(const BackArgs a) {
+template <typename T, int NV>
+__global__ void __launch_bounds__(512) norm_back_kernel(const BackArgs a, int group_threads) {
   pdl_launch_dependents();
   pdl_wait_prior();
   __shared__ float part[2][32];
-  extern __shared__ float s_acc[];   // kWarpRow: [8 warps][k]
-  const int lane = threadIdx.x & 31;
-  const int t = kWarpRow ? lane : static_cast<int>(threadIdx.x);
-  const int nt = kWarpRow ? 32 : static_cast<int>(blockDim.x);
-  const int per_cta = kWarpRow ? static_cast<int>(blockDim.x >> 5) : 1;
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * per_cta + (kWarpRow ? threadIdx.x >> 5 : 0);
-  const int64_t step = static_cast<int64_t>(gridDim.x) * per_cta;
+  extern __shared__ float s_acc[];   // [groups][k], one group: unused
+  const int groups = static_cast<int>(blockDim.x) / group_threads;
+  const int grp = static_cast<int>(threadIdx.x) / group_threads;
+  const int t = static_cast<int>(threadIdx.x) - grp * group_threads;
+  const int warps = group_threads >> 5;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * groups + grp;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
   const int c_end = static_cast<int>(a.k / 8);
   const float inv_k = __fdiv_rn(1.0f, static_cast<float>(a.k));
   const bool has_dh = a.dh != nullptr;
@@ -375,37 +420,38 @@ norm_back_kernel(const BackArgs a) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[i][j] = 0.0f;
 
-  Vec8<T> dy[NV], h[NV], dh[NV];
+  // the next row's dy and h are loaded before this one is reduced, where the
+  // registers allow
+  constexpr bool kAhead = NV <= 2;
+  Vec8<T> dy[NV], h[NV];
   float rs_next = 0.0f;
   auto load = [&](int64_t row) {
     const int64_t base = row * a.k;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = t + i * nt;
+      const int c = t + i * group_threads;
+      dy[i].zero();
+      h[i].zero();
       if (c < c_end) {
         dy[i].load(static_cast<const T*>(a.dy) + base + 8 * c);
         h[i].load(static_cast<const T*>(a.h) + base + 8 * c);
-        if (has_dh) dh[i].load(static_cast<const T*>(a.dh) + base + 8 * c);
-      } else {
-        dy[i].zero();
-        h[i].zero();
-        if (has_dh) dh[i].zero();
       }
     }
     rs_next = a.rstd[row];
   };
-  if (first < a.m) load(first);
+  if (kAhead && first < a.m) load(first);
   uint32_t buf = 0;
   for (int64_t row = first; row < a.m; row += step, buf ^= 1u) {
+    if (!kAhead) load(row);
     const float rs = rs_next;
-    Vec8<T> cdy[NV], ch[NV], cdh[NV];
+    Vec8<T> cdy[NV], ch[NV], dh[NV];
     float dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = t + i * nt;
+      const int c = t + i * group_threads;
       cdy[i] = dy[i];
       ch[i] = h[i];
-      if (has_dh) cdh[i] = dh[i];
+      if (kAhead && has_dh && c < c_end) dh[i].load(static_cast<const T*>(a.dh) + row * a.k + 8 * c);
       Vec8<T> g;
       g.zero();
       if (c < c_end) g.load_cached(static_cast<const T*>(a.gamma) + 8 * c);
@@ -415,65 +461,57 @@ norm_back_kernel(const BackArgs a) {
       g.get(fg);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float xh = fh[j] * rs;
-        acc[i][j] = __fmaf_rn(fd[j], xh, acc[i][j]);
-        dot = __fmaf_rn(fd[j] * fg[j], xh, dot);
+        const float p = fd[j] * fh[j];
+        acc[i][j] = __fmaf_rn(p, rs, acc[i][j]);
+        dot = __fmaf_rn(p, fg[j], dot);
       }
     }
-    if (row + step < a.m) load(row + step);
-    dot = row_sum<kWarpRow>(dot, part, buf);
-    const float mean = dot * inv_k;
+    if (kAhead && row + step < a.m) load(row + step);
+    dot = row_sum<false>(dot, part[buf] + grp * warps, t >> 5, warps, 1 + grp);
+    const float coef = -(dot * inv_k) * rs * rs * rs;
     T* out = static_cast<T*>(a.dx) + row * a.k;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = t + i * nt;
+      const int c = t + i * group_threads;
       if (c < c_end) {
         Vec8<T> g, o;
         g.load_cached(static_cast<const T*>(a.gamma) + 8 * c);
+        if (!kAhead && has_dh) dh[i].load(static_cast<const T*>(a.dh) + row * a.k + 8 * c);
         float fd[8], fh[8], fg[8], fo[8];
         cdy[i].get(fd);
         ch[i].get(fh);
         g.get(fg);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float xh = fh[j] * rs;
-          fo[j] = rs * (fd[j] * fg[j] - xh * mean);
-        }
         if (has_dh) {
-          float f[8];
-          cdh[i].get(f);
+          dh[i].get(fo);
+        } else {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) fo[j] += f[j];
+          for (int j = 0; j < 8; ++j) fo[j] = 0.0f;
         }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          fo[j] = __fmaf_rn(fd[j] * fg[j], rs, __fmaf_rn(fh[j], coef, fo[j]));
         o.set(fo);
         o.store(out + 8 * c);
       }
     }
   }
   float* dst = a.part + static_cast<int64_t>(blockIdx.x) * a.k;
-  if constexpr (kWarpRow) {
-    // the warps' sums, added in warp order
+  float* sums = groups > 1 ? s_acc + grp * a.k : dst;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = t + i * nt;
-      if (c < c_end)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s_acc[(threadIdx.x >> 5) * a.k + 8 * c + j] = acc[i][j];
+  for (int i = 0; i < NV; ++i) {
+    const int c = t + i * group_threads;
+    if (c < c_end) {
+      float4* q = reinterpret_cast<float4*>(sums + 8 * c);
+      q[0] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+      q[1] = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
     }
+  }
+  if (groups > 1) {
     __syncthreads();
     for (int c = threadIdx.x; c < a.k; c += blockDim.x) {
       float s = 0.0f;
-      for (int w = 0; w < per_cta; ++w) s += s_acc[w * a.k + c];
+      for (int i = 0; i < groups; ++i) s += s_acc[i * a.k + c];
       dst[c] = s;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = t + i * nt;
-      if (c < c_end) {
-        reinterpret_cast<float4*>(dst + 8 * c)[0] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
-        reinterpret_cast<float4*>(dst + 8 * c)[1] = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
-      }
     }
   }
 }
@@ -554,10 +592,14 @@ static int round32(int64_t v) { return static_cast<int>((v + 31) / 32 * 32); }
 template <typename T, int OUT>
 static sp24_status launch_norm(const NormArgs& a, cudaStream_t s) {
   const int64_t c = a.k / 8;   // vectors of a row
-  if (c <= 32) return launch_norm_t<T, OUT, 1, true, 256, 4>(a, 256, s);
-  if (c <= 64) return launch_norm_t<T, OUT, 2, true, 256, 4>(a, 256, s);
-  if (c <= 128) return launch_norm_t<T, OUT, 4, true, 256, 2>(a, 256, s);
-  if (c <= 1024 && a.m <= 2 * sm_count())
+  if (c <= 32) return launch_norm_t<T, OUT, 1, true, 256, 1>(a, 256, s);
+  if (c <= 64) return launch_norm_t<T, OUT, 2, true, 256, 1>(a, 256, s);
+  // One vector a thread where a block can have that many threads: always for
+  // float32 (2000 x 4096 with residual: 19.6 us, two vectors 23.6) and up to
+  // 1024 columns (4096 x 768: 5.9 us, a warp with four vectors 7.2), for bf16
+  // otherwise only when the rows are few; with many rows two vectors a thread keep more
+  // bytes in flight (8192 x 4096: 39.7 us, one vector 45.1, four 41.8).
+  if (c <= 1024 && (c <= 128 || sizeof(T) == 4 || a.m <= 2 * sm_count()))
     return launch_norm_t<T, OUT, 1, false, 1024, 1>(a, round32(c), s);
   if (c > 1024 && c <= 1536 && sizeof(T) == 4)
     return launch_norm_t<T, OUT, 2, false, 768, 2>(a, round32((c + 1) / 2), s);
@@ -583,32 +625,39 @@ static sp24_status launch_quantize(const QuantArgs& a, cudaStream_t s) {
 // Rows of the dgamma workspace: at most this many blocks run the backward.
 constexpr int64_t kBackMaxCtas = 640;
 
-template <typename T, int NV, bool kWarpRow>
-static sp24_status launch_back_t(const BackArgs& a, int threads, float* dgamma, cudaStream_t s) {
-  auto kern = norm_back_kernel<T, NV, kWarpRow>;
+template <typename T, int NV>
+static sp24_status launch_back_t(const BackArgs& a, int group_threads, float* dgamma,
+                                 cudaStream_t s) {
+  auto kern = norm_back_kernel<T, NV>;
   static Occupancy occ;
-  const size_t smem = kWarpRow ? static_cast<size_t>(threads / 32) * a.k * 4 : 0;
+  // as many groups as 512 threads hold (their hardware barriers are 1 .. 15),
+  // fewer where the rows are few
+  int64_t groups = 512 / group_threads;
+  if (groups > 15) groups = 15;
+
+  const int64_t spread = (a.m + sm_count() - 1) / sm_count();
+  if (groups > spread) groups = spread < 1 ? 1 : spread;
+  const int threads = static_cast<int>(groups) * group_threads;
+  const size_t smem = groups > 1 ? static_cast<size_t>(groups) * a.k * 4 : 0;
   int per_sm = 0;
   SP24_TRY(resident_blocks(reinterpret_cast<const void*>(kern), occ, threads, smem, &per_sm));
-  const int64_t per_cta = kWarpRow ? threads / 32 : 1;
-  int64_t ctas = (a.m + per_cta - 1) / per_cta;
+  int64_t ctas = (a.m + groups - 1) / groups;
   const int64_t cap = static_cast<int64_t>(sm_count()) * per_sm;
   if (ctas > cap) ctas = cap;
   if (ctas > kBackMaxCtas) ctas = kBackMaxCtas;
   if (ctas > 0)
-    SP24_TRY(launch_kernel(kern, dim3(static_cast<unsigned>(ctas)), dim3(threads), smem, s, 1, a));
+    SP24_TRY(launch_kernel(kern, dim3(static_cast<unsigned>(ctas)), dim3(threads), smem, s, 1, a,
+                           group_threads));
   return launch_kernel(dgamma_kernel, dim3(static_cast<unsigned>((a.k + 31) / 32)), dim3(256), 0, s,
                        1, static_cast<const float*>(a.part), static_cast<int>(ctas), a.k, dgamma);
 }
 
 template <typename T>
 static sp24_status launch_back(const BackArgs& a, float* dgamma, cudaStream_t s) {
-  const int64_t c = a.k / 8;
-  if (c <= 32) return launch_back_t<T, 1, true>(a, 256, dgamma, s);
-  if (c <= 64) return launch_back_t<T, 2, true>(a, 256, dgamma, s);
-  if (c <= 128) return launch_back_t<T, 4, true>(a, 256, dgamma, s);
-  if (c <= 1024) return launch_back_t<T, 2, false>(a, round32((c + 1) / 2), dgamma, s);
-  return launch_back_t<T, 4, false>(a, round32((c + 3) / 4), dgamma, s);
+  const int64_t c = a.k / 8;   // vectors of a row
+  if (c <= 256) return launch_back_t<T, 1>(a, round32(c), dgamma, s);
+  if (c <= 1024) return launch_back_t<T, 2>(a, round32((c + 1) / 2), dgamma, s);
+  return launch_back_t<T, 4>(a, round32((c + 3) / 4), dgamma, s);
 }
 
 }  // namespace sp24
