@@ -418,7 +418,8 @@ sp24_status sp24_gemm_fp8(const void* X, const uint8_t* e_x, int64_t M, int64_t 
 /* RMS norm of the residual stream with the operand of the next product as its
  * output, in one pass:
  *   h = X + R rounded to the stream's type (h = X without R);
- *   s = 1 / sqrt(mean over the row of h^2 + eps), y = (h * s) * gamma, fp32;
+ *   s = 1 / sqrt(mean over the row of h^2 + eps), y = h * gamma * s in fp32
+ *   (one rounding; squares are summed in fp32 within a warp, in fp64 across);
  *   out_dtype SP24_FP8:  Y e4m3 [M][K] with the scales e_y (as sp24_quantize_fp8
  *                        of y: the operand of sp24_gemm_fp8);
  *             SP24_INT8: Y int8 [M][K] = clamp(rint(y / *s_x), -127, 127), float32

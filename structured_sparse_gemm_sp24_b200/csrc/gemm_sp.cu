@@ -121,21 +121,25 @@ int pair_tokens(int impl) {
 // Estimated run time (us, B200 under load) of a persistent variant: waves of
 // output tiles over the SMs (resident pairs) x per-tile time, i.e. k-blocks x
 // the measured cost of one k-block plus the part of the epilogue the variant
-// cannot overlap with the next tile.  Used only to rank the variants.
-double est_time(int impl, int64_t m, int64_t n, int kblocks, int sms, int pairs) {
+// cannot overlap with the next tile.  Used only to rank the variants.  e4m3:
+// 0.59, 0.535 and 0.515 us a k-block of 256-, 240- and 224-token tiles (8192 x
+// 11008 x 4096: 194, 180 us; 8192 x 4096 x 4096: 73, 68, 66 us; the first has
+// room for three ring stages only).
+double est_time(int impl, int64_t m, int64_t n, int kblocks, int sms, int pairs, bool fp8) {
   const auto waves = [](int64_t tiles, int64_t units) {
     return static_cast<double>((tiles + units - 1) / units);
   };
   const double kb = kblocks;
   const int64_t prow = (n + 255) / 256;
+  const double c256 = fp8 ? 0.59 : 0.50, c240 = fp8 ? 0.535 : 0.50, c224 = fp8 ? 0.515 : 0.50;
   switch (impl) {
     case kPair256:   // one accumulator: the next tile waits for the epilogue's
                      // tensor-memory loads (~0.8 us a tile, measured)
-      return waves(prow * ((m + 255) / 256), pairs) * (0.50 * kb + 0.8);
+      return waves(prow * ((m + 255) / 256), pairs) * (c256 * kb + 0.8);
     case kPair240:   // two accumulators: only the last drain is exposed
-      return waves(prow * ((m + 239) / 240), pairs) * std::max(0.50 * kb, 1.5) + 2.0;
+      return waves(prow * ((m + 239) / 240), pairs) * std::max(c240 * kb, 1.5) + 2.0;
     case kPair224:
-      return waves(prow * ((m + 223) / 224), pairs) * std::max(0.50 * kb, 1.4) + 2.0;
+      return waves(prow * ((m + 223) / 224), pairs) * std::max(c224 * kb, 1.4) + 2.0;
     default:         // 128 x 128 single-SM tile, two accumulators
       return waves(((n + 127) / 128) * ((m + 127) / 128), sms) * std::max(0.48 * kb, 1.6);
   }
@@ -204,9 +208,9 @@ sp24_status make_plan(int64_t m, int64_t n, int kblocks, int dtype, Plan* p) {
     if (impl < 0) {
       impl = kSingle;   // pair tiles need both dimensions to fill them
       if (m >= 256 && n >= 256) {
-        double best = fp8 ? 1e30 : est_time(kSingle, m, n, kblocks, sms, pairs);
+        double best = fp8 ? 1e30 : est_time(kSingle, m, n, kblocks, sms, pairs, false);
         for (int c : {kPair256, kPair240, kPair224}) {
-          const double t = est_time(c, m, n, kblocks, sms, pairs);
+          const double t = est_time(c, m, n, kblocks, sms, pairs, fp8);
           if (t < best) {
             best = t;
             impl = c;

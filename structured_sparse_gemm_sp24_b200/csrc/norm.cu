@@ -3,8 +3,8 @@
 // quantisation of an activation that no norm precedes (sp24_quantize_fp8).
 //
 //   h = round(x + r)                       the residual stream as stored
-//   s = 1 / sqrt(mean(h^2) + eps)          fp32 sums
-//   y = (h * s) * gamma                    fp32
+//   s = 1 / sqrt(mean(h^2) + eps)          fp32 within a warp, fp64 across
+//   y = h * gamma * s                      rounded once to fp32
 //   e4m3: one power-of-two scale per row and 128 columns (fp8.cuh)
 //   int8: clamp(rint(y / s_x), -127, 127), the rule of sp24_quantize
 //   bf16: y rounded
@@ -21,6 +21,46 @@
 #include "sp24_host.h"
 
 namespace sp24 {
+
+// ------------------------------------------------------------ pairs of fp32
+// The arithmetic works on pairs (one instruction for two elements): these
+// kernels spend about as long issuing as waiting for memory.
+struct Pair {
+  uint64_t v;
+};
+__device__ __forceinline__ Pair pair(float a, float b) {
+  Pair r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ Pair pair(float a) { return pair(a, a); }
+__device__ __forceinline__ void split(Pair p, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p.v));
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+  Pair r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  Pair r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ Pair fma2_rz(Pair a, Pair b, Pair c) {
+  Pair r;
+  asm("fma.rz.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
+// Eight e4m3 codes of four pairs times a power of two.
+__device__ __forceinline__ uint2 e4m3x8(const Pair (&f)[4], float scale) {
+  const Pair s = pair(scale);
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) split(mul2(f[i], s), y[2 * i], y[2 * i + 1]);
+  return make_uint2(e4m3x4(y[0], y[1], y[2], y[3]), e4m3x4(y[4], y[5], y[6], y[7]));
+}
 
 // ------------------------------------------------------- 8-element vectors
 // Loads that leave no line in L1 (each element is read once).
@@ -50,6 +90,12 @@ struct Vec8<__nv_bfloat16> {
       f[2 * i] = __uint_as_float(w[i] << 16);
       f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
     }
+  }
+  __device__ __forceinline__ void get(Pair (&f)[4]) const {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      f[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
   }
   // += v, each sum rounded once (the bf16 adder rounds the exact sum)
   __device__ __forceinline__ void add(const Vec8& v) {
@@ -90,6 +136,12 @@ struct Vec8<float> {
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
   }
+  __device__ __forceinline__ void get(Pair (&f)[4]) const {
+    float g[8];
+    get(g);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = pair(g[2 * i], g[2 * i + 1]);
+  }
   __device__ __forceinline__ void add(const Vec8& v) {
     float f[8], g[8];
     get(f);
@@ -127,16 +179,22 @@ __device__ __forceinline__ uint32_t block_max(uint32_t v) {
 // warp's by shuffles, then the warps' in order through `part`, of which two
 // rows' buffers alternate so that one barrier (hardware barrier `bar`, of the
 // row's threads) is enough.
-template <bool kWarpRow>
-__device__ __forceinline__ float row_sum(float v, float* part, int warp, int warps, uint32_t bar) {
+// S is the type of the sum across warps: double keeps the last additions, whose
+// roundings no averaging hides, out of the result.
+template <bool kWarpRow, typename S>
+__device__ __forceinline__ S row_sum(float v, S* part, int warp, int warps, uint32_t bar) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  if constexpr (kWarpRow) return v;
-  if ((threadIdx.x & 31) == 0) part[warp] = v;
+  if constexpr (kWarpRow) return static_cast<S>(v);
+  if ((threadIdx.x & 31) == 0) part[warp] = static_cast<S>(v);
   named_barrier(bar, 32 * warps);
-  float t = 0.0f;
-  for (int i = 0; i < warps; ++i) t += part[i];
-  return t;
+  S t[4] = {S(0), S(0), S(0), S(0)};
+  for (int i = 0; i < warps; i += 4) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (i + j < warps) t[j] += part[i + j];
+  }
+  return (t[0] + t[1]) + (t[2] + t[3]);
 }
 
 // ------------------------------------------------------------------ forward
@@ -150,6 +208,7 @@ struct NormArgs {
   float* rstd;          // optional
   const float* s_x;     // int8: the given scale
   int64_t m, k;
+  double inv_k;         // 1 / k
   float eps;
   int scale_cols;
 };
@@ -157,14 +216,61 @@ struct NormArgs {
 // h of one vector: x + r rounded to the stream's type (x without r), and its
 // squares added to `sum` in fp32.  The norm is that of the stored sum.
 template <typename T>
-__device__ __forceinline__ Vec8<T> norm_sum(const Vec8<T>& x, const Vec8<T>& r, bool res, float& sum) {
+__device__ __forceinline__ Vec8<T> norm_sum(const Vec8<T>& x, const Vec8<T>& r, bool res, Pair& sum) {
   Vec8<T> h = x;
   if (res) h.add(r);
-  float f[8];
+  Pair f[4];
   h.get(f);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) sum = __fmaf_rn(f[j], f[j], sum);
+  for (int j = 0; j < 4; ++j) sum = fma2(f[j], f[j], sum);
   return h;
+}
+
+// y = h * gamma * s of one vector, rounded once.  s comes as hi + lo; the product
+// of two bf16 values is exact in fp32, that of two floats is taken with its
+// remainder.
+//
+// kOdd: rounded to odd (truncated, last bit set), for a y that is rounded again
+// to a code: every border between codes is an even fp32 number, so y stays on
+// the side of the border that the exact product is on, and only the error of s
+// can still move a code (8192 x 4096: 1 to 23 of 33.5 million codes differ from
+// those of 64 bits, 20 to 27 with y rounded to nearest, 19 to 38 in plain fp32).
+// `last` is the bit to set in both halves: an inexact product is needed, which
+// lo != 0 makes it, so it is 0 for a row with lo == 0.  A zero becomes the
+// smallest subnormal.
+template <bool kOdd>
+__device__ __forceinline__ Pair norm_round(Pair p, Pair s, Pair rest, uint64_t last) {
+  if constexpr (!kOdd) return fma2(p, s, rest);
+  Pair y = fma2_rz(p, s, rest);
+  y.v |= last;
+  return y;
+}
+template <bool kOdd>
+__device__ __forceinline__ void norm_scale(const Vec8<__nv_bfloat16>& h, const Vec8<__nv_bfloat16>& g,
+                                           float2 s, Pair (&y)[4]) {
+  const uint64_t last = s.y != 0.0f ? 0x0000000100000001ull : 0ull;
+  Pair fg[4];
+  h.get(y);
+  g.get(fg);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const Pair p = mul2(y[j], fg[j]);
+    y[j] = norm_round<kOdd>(p, pair(s.x), mul2(p, pair(s.y)), last);
+  }
+}
+template <bool kOdd>
+__device__ __forceinline__ void norm_scale(const Vec8<float>& h, const Vec8<float>& g, float2 s,
+                                           Pair (&y)[4]) {
+  const uint64_t last = s.y != 0.0f ? 0x0000000100000001ull : 0ull;
+  Pair fg[4];
+  h.get(y);
+  g.get(fg);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const Pair p = mul2(y[j], fg[j]);
+    const Pair e = fma2(y[j], fg[j], mul2(p, pair(-1.0f)));
+    y[j] = norm_round<kOdd>(p, pair(s.x), fma2(p, pair(s.y), mul2(e, pair(s.x))), last);
+  }
 }
 
 // y of one vector (columns 8c ..) of row `row` and its output.  All lanes of a
@@ -172,22 +278,21 @@ __device__ __forceinline__ Vec8<T> norm_sum(const Vec8<T>& x, const Vec8<T>& r, 
 // 128-column block.
 template <typename T, int OUT>
 __device__ __forceinline__ void norm_out(const NormArgs& a, const Vec8<T>& h, const Vec8<T>& g,
-                                         float rs, int64_t row, int c, bool ok, float sx, float rsx) {
-  float f[8], fg[8];
-  h.get(f);
-  g.get(fg);
+                                         float2 rs, int64_t row, int c, bool ok, float sx, float rsx) {
+  Pair y[4];
+  norm_scale<OUT == SP24_FP8>(h, g, rs, y);
+  float f[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) f[j] = __fmul_rn(__fmul_rn(f[j], rs), fg[j]);
+  for (int j = 0; j < 4; ++j) split(y[j], f[2 * j], f[2 * j + 1]);
   const int64_t at = row * a.k + 8 * c;
   if constexpr (OUT == SP24_FP8) {
     // (a NaN statistic makes NaNs of the zeros past the row)
-    const uint32_t amax = block_max(ok ? amax8(f) : 0u);
+    uint32_t amax = block_max(ok ? amax8(f) : 0u);
+    if (amax == 1u) amax = 0u;   // a block of zeros, rounded to odd
     const uint32_t byte = scale_byte(amax);
     const float inv = scale_inverse(byte == kScaleNan ? kScaleOne : byte);
     if (ok) {
-      uint2 q;
-      q.x = e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
-      q.y = e4m3x4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv);
+      uint2 q = e4m3x8(y, inv);
       if (byte == kScaleNan) q.x = q.y = kCodeNan4;
       *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.y) + at) = q;
       if ((threadIdx.x & 15) == 0) a.e[row * a.scale_cols + (c >> 4)] = static_cast<uint8_t>(byte);
@@ -210,14 +315,24 @@ __device__ __forceinline__ void norm_out(const NormArgs& a, const Vec8<T>& h, co
   }
 }
 
-__device__ __forceinline__ float norm_rstd(float sum, const NormArgs& a) {
-  return __frsqrt_rn(__fadd_rn(__fdiv_rn(sum, static_cast<float>(a.k)), a.eps));
+// 1 / sqrt(mean + eps) as hi + lo: the rounded root of the rounded argument and
+// one Newton step from its residual 1 - v hi^2, formed with exact products.  A
+// root that is 0, infinite or NaN stands as it is.
+__device__ __forceinline__ float2 norm_rstd(double sum, const NormArgs& a) {
+  const double v = __fma_rn(sum, a.inv_k, static_cast<double>(a.eps));
+  const float vh = __double2float_rn(v);
+  const float vl = __double2float_rn(v - static_cast<double>(vh));
+  const float r = __frsqrt_rn(vh);
+  const float t = __fmul_rn(r, r), tl = __fmaf_rn(r, r, -t);
+  const float e = __fmaf_rn(-vl, t, __fmaf_rn(-vh, tl, __fmaf_rn(-vh, t, 1.0f)));
+  const float lo = __fmul_rn(0.5f * r, e);
+  return make_float2(r, fabsf(lo) < r ? lo : 0.0f);   // (false for inf, NaN)
 }
 
 // Per row: 1 / rms, and (e4m3) the padding of the scale row, by thread t of the row.
 template <int OUT>
-__device__ __forceinline__ void norm_row_end(const NormArgs& a, int64_t row, int t, float rs) {
-  if (a.rstd != nullptr && t == 0) a.rstd[row] = rs;
+__device__ __forceinline__ void norm_row_end(const NormArgs& a, int64_t row, int t, float2 rs) {
+  if (a.rstd != nullptr && t == 0) a.rstd[row] = rs.x + rs.y;
   if constexpr (OUT == SP24_FP8) {
     const int kb = static_cast<int>((a.k + 127) >> 7);
     if (t < a.scale_cols - kb) a.e[row * a.scale_cols + kb + t] = static_cast<uint8_t>(kScaleOne);
@@ -229,7 +344,7 @@ template <typename T, int OUT, int NV, bool kWarpRow, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) norm_kernel(const NormArgs a) {
   pdl_launch_dependents();
   pdl_wait_prior();
-  __shared__ float part[2][32];
+  __shared__ double part[2][32];
   const int t = kWarpRow ? static_cast<int>(threadIdx.x & 31) : static_cast<int>(threadIdx.x);
   const int nt = kWarpRow ? 32 : static_cast<int>(blockDim.x);
   const int per_cta = kWarpRow ? static_cast<int>(blockDim.x >> 5) : 1;
@@ -263,15 +378,18 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_kernel(const NormArgs a) {
   for (int64_t row = first; row < a.m; row += step, buf ^= 1u) {
     if (!kAhead) load(row);
     Vec8<T> h[NV];
-    float sum = 0.0f;
+    Pair sum2 = pair(0.0f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = t + i * nt;
-      h[i] = norm_sum<T>(x[i], r[i], res, sum);
+      h[i] = norm_sum<T>(x[i], r[i], res, sum2);
       if (a.h != nullptr && c < c_end) h[i].store(static_cast<T*>(a.h) + row * a.k + 8 * c);
     }
     if (kAhead && row + step < a.m) load(row + step);
-    const float rs = norm_rstd(row_sum<kWarpRow>(sum, part[buf], threadIdx.x >> 5, blockDim.x >> 5, 0), a);
+    float sum, odd;
+    split(sum2, sum, odd);
+    const float2 rs = norm_rstd(
+        row_sum<kWarpRow, double>(sum + odd, part[buf], threadIdx.x >> 5, blockDim.x >> 5, 0), a);
     norm_row_end<OUT>(a, row, t, rs);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -298,7 +416,7 @@ constexpr int kQuantThreads = 256;
 // mul = floor(2^32 (2^l - d) / d) + 1 it is (mulhi(n, mul) + n) >> l.
 struct FastDiv {
   uint32_t mul, shift;
-  explicit FastDiv(uint32_t d = 1) {
+  FastDiv(uint32_t d = 1) {
     shift = 0;
     while ((uint64_t(1) << shift) < d) ++shift;
     mul = static_cast<uint32_t>((((uint64_t(1) << shift) - d) << 32) / d + 1);
@@ -357,11 +475,9 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_fp8_kernel(const Quant
     const uint32_t byte = scale_byte(amax);
     const float inv = scale_inverse(byte == kScaleNan ? kScaleOne : byte);
     if (at[u] >= 0) {
-      float f[8];
+      Pair f[4];
       x[u].get(f);
-      uint2 q;
-      q.x = e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
-      q.y = e4m3x4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv);
+      uint2 q = e4m3x8(f, inv);
       if (byte == kScaleNan) q.x = q.y = kCodeNan4;
       *reinterpret_cast<uint2*>(a.y + at[u]) = q;
       if (t == 0) {   // the scale, and after a row's last block the row's padding
@@ -414,11 +530,11 @@ __global__ void __launch_bounds__(512) norm_back_kernel(const BackArgs a, int gr
   const float inv_k = __fdiv_rn(1.0f, static_cast<float>(a.k));
   const bool has_dh = a.dh != nullptr;
 
-  float acc[NV][8];
+  Pair acc[NV][4];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[i][j] = 0.0f;
+    for (int j = 0; j < 4; ++j) acc[i][j] = pair(0.0f);
 
   // the next row's dy and h are loaded before this one is reduced, where the
   // registers allow
@@ -445,7 +561,7 @@ __global__ void __launch_bounds__(512) norm_back_kernel(const BackArgs a, int gr
     if (!kAhead) load(row);
     const float rs = rs_next;
     Vec8<T> cdy[NV], ch[NV], dh[NV];
-    float dot = 0.0f;
+    Pair dot2 = pair(0.0f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = t + i * group_threads;
@@ -455,19 +571,21 @@ __global__ void __launch_bounds__(512) norm_back_kernel(const BackArgs a, int gr
       Vec8<T> g;
       g.zero();
       if (c < c_end) g.load_cached(static_cast<const T*>(a.gamma) + 8 * c);
-      float fd[8], fh[8], fg[8];
+      Pair fd[4], fh[4], fg[4];
       cdy[i].get(fd);
       ch[i].get(fh);
       g.get(fg);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float p = fd[j] * fh[j];
-        acc[i][j] = __fmaf_rn(p, rs, acc[i][j]);
-        dot = __fmaf_rn(p, fg[j], dot);
+      for (int j = 0; j < 4; ++j) {
+        const Pair p = mul2(fd[j], fh[j]);
+        acc[i][j] = fma2(p, pair(rs), acc[i][j]);
+        dot2 = fma2(p, fg[j], dot2);
       }
     }
     if (kAhead && row + step < a.m) load(row + step);
-    dot = row_sum<false>(dot, part[buf] + grp * warps, t >> 5, warps, 1 + grp);
+    float dot, odd;
+    split(dot2, dot, odd);
+    dot = row_sum<false, float>(dot + odd, part[buf] + grp * warps, t >> 5, warps, 1 + grp);
     const float coef = -(dot * inv_k) * rs * rs * rs;
     T* out = static_cast<T*>(a.dx) + row * a.k;
 #pragma unroll
@@ -477,7 +595,7 @@ __global__ void __launch_bounds__(512) norm_back_kernel(const BackArgs a, int gr
         Vec8<T> g, o;
         g.load_cached(static_cast<const T*>(a.gamma) + 8 * c);
         if (!kAhead && has_dh) dh[i].load(static_cast<const T*>(a.dh) + row * a.k + 8 * c);
-        float fd[8], fh[8], fg[8], fo[8];
+        Pair fd[4], fh[4], fg[4], fo[4];
         cdy[i].get(fd);
         ch[i].get(fh);
         g.get(fg);
@@ -485,12 +603,14 @@ __global__ void __launch_bounds__(512) norm_back_kernel(const BackArgs a, int gr
           dh[i].get(fo);
         } else {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) fo[j] = 0.0f;
+          for (int j = 0; j < 4; ++j) fo[j] = pair(0.0f);
         }
+        float f[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          fo[j] = __fmaf_rn(fd[j] * fg[j], rs, __fmaf_rn(fh[j], coef, fo[j]));
-        o.set(fo);
+        for (int j = 0; j < 4; ++j)
+          split(fma2(mul2(fd[j], fg[j]), pair(rs), fma2(fh[j], pair(coef), fo[j])), f[2 * j],
+                f[2 * j + 1]);
+        o.set(f);
         o.store(out + 8 * c);
       }
     }
@@ -501,9 +621,12 @@ __global__ void __launch_bounds__(512) norm_back_kernel(const BackArgs a, int gr
   for (int i = 0; i < NV; ++i) {
     const int c = t + i * group_threads;
     if (c < c_end) {
+      float f[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) split(acc[i][j], f[2 * j], f[2 * j + 1]);
       float4* q = reinterpret_cast<float4*>(sums + 8 * c);
-      q[0] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
-      q[1] = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
+      q[0] = make_float4(f[0], f[1], f[2], f[3]);
+      q[1] = make_float4(f[4], f[5], f[6], f[7]);
     }
   }
   if (groups > 1) {
@@ -692,6 +815,7 @@ sp24_status sp24_rmsnorm_quant(const void* X, const void* R, const void* gamma, 
   a.s_x = s_x;
   a.m = M;
   a.k = K;
+  a.inv_k = 1.0 / static_cast<double>(K);
   a.eps = eps;
   a.scale_cols = static_cast<int>(4 * ((K + 511) / 512));
   return x_dtype == SP24_F32 ? launch_norm_out<float>(a, out_dtype, as_stream(stream))
