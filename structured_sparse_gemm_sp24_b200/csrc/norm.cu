@@ -188,6 +188,13 @@ __device__ __forceinline__ S row_sum(float v, S* part, int warp, int warps, uint
   if constexpr (kWarpRow) return static_cast<S>(v);
   if ((threadIdx.x & 31) == 0) part[warp] = static_cast<S>(v);
   named_barrier(bar, 32 * warps);
+  if (warps > 8) {   // one value a lane, and shuffles, instead of a long chain
+    const int lane = threadIdx.x & 31;
+    S u = lane < warps ? part[lane] : S(0);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xFFFFFFFFu, u, o);
+    return u;
+  }
   S t[4] = {S(0), S(0), S(0), S(0)};
   for (int i = 0; i < warps; i += 4) {
 #pragma unroll
