@@ -48,13 +48,13 @@ __device__ __forceinline__ uint32_t select2_mag(const uint4& q, uint32_t& top) {
   const uint32_t x = q.x & kM, y = q.y & kM, z = q.z & kM, w = q.w & kM;
   const uint32_t p0 = __byte_perm(x, z, 0x5410), p1 = __byte_perm(x, z, 0x7632);
   const uint32_t p2 = __byte_perm(y, w, 0x5410), p3 = __byte_perm(y, w, 0x7632);
-  const uint32_t a = __vmaxu2(p0, p1), b = __vminu2(p0, p1);
-  const uint32_t c = __vmaxu2(p2, p3), d = __vminu2(p2, p3);
+  const uint32_t a = max_u16x2(p0, p1), b = min_u16x2(p0, p1);
+  const uint32_t c = max_u16x2(p2, p3), d = min_u16x2(p2, p3);
   const uint32_t ge01 = (p0 | kG) - p1;   // flags in bits 15 and 31
   const uint32_t ge23 = (p2 | kG) - p3;
   const uint32_t first = (b | kG) - c;    // keep 0, 1
   const uint32_t not_last = (a | kG) - d; // clear: keep 2, 3
-  top = __vmaxu2(a, c);
+  top = max_u16x2(a, c);
   const uint32_t lo0 = ~first & not_last & ~ge01, lo1 = ~not_last;
   const uint32_t hi0 = first | ~not_last | ~ge23, hi1 = ~first;
   const uint32_t t = ((lo0 >> 15) & 0x00010001u) | ((lo1 >> 14) & 0x00020002u) |
@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kConvThreads) convert_fp8_kernel(const Convert
     if constexpr (kPrune && !kWanda && !kMaskIn) {
       uint32_t top;
       code = select2_mag(q[j], top);       // (zeros keep 0, 1)
-      amax = __vmaxu2(amax, top);          // both halves hold magnitudes
+      amax = max_u16x2(amax, top);          // both halves hold magnitudes
     } else {
       uint32_t keep = 0x33u;
       if (j < rows) {
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kConvThreads) convert_fp8_kernel(const Convert
     p0[j] = gather_code(q[j].x, q[j].y, code & 15u);
     p1[j] = gather_code(q[j].z, q[j].w, code >> 4);
     if constexpr (!(kPrune && !kWanda && !kMaskIn))
-      amax = __vmaxu2(amax, __vmaxu2(p0[j] & 0x7FFF7FFFu, p1[j] & 0x7FFF7FFFu));
+      amax = max_u16x2(amax, max_u16x2(p0[j] & 0x7FFF7FFFu, p1[j] & 0x7FFF7FFFu));
     s_meta[(m0 + 16 * j) * 16 + bb] = static_cast<uint8_t>(code);
     if (a.mask_out)
       s_mask[(m0 + 16 * j) * 16 + bb] = static_cast<uint8_t>(
@@ -139,16 +139,15 @@ __global__ void __launch_bounds__(kConvThreads) convert_fp8_kernel(const Convert
 #pragma unroll
   for (int i = 0; i < kConvThreads / 32; ++i) amax = max(amax, s_max[i]);
   const uint32_t byte = scale_byte(amax);
-  const float inv = scale_inverse(byte == kScaleNan ? kScaleOne : byte);
+  const float inv = scale_inverse(byte);
   uint32_t* dst = a.vals + row0 * kvec + v;
 #pragma unroll
   for (int j = 0; j < kConvRows; ++j) {
     if (j < rows) {
-      uint32_t c = e4m3x4(__uint_as_float(p0[j] << 16) * inv,
+      const uint32_t c = e4m3x4(__uint_as_float(p0[j] << 16) * inv,
                           __uint_as_float(p0[j] & 0xFFFF0000u) * inv,
                           __uint_as_float(p1[j] << 16) * inv,
                           __uint_as_float(p1[j] & 0xFFFF0000u) * inv);
-      if (byte == kScaleNan) c = kCodeNan4;
       __stcs(dst + 16 * j * kvec, c);
     }
   }

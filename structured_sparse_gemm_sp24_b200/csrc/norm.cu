@@ -297,10 +297,9 @@ __device__ __forceinline__ void norm_out(const NormArgs& a, const Vec8<T>& h, co
     uint32_t amax = block_max(ok ? amax8(f) : 0u);
     if (amax == 1u) amax = 0u;   // a block of zeros, rounded to odd
     const uint32_t byte = scale_byte(amax);
-    const float inv = scale_inverse(byte == kScaleNan ? kScaleOne : byte);
+    const float inv = scale_inverse(byte);
     if (ok) {
-      uint2 q = e4m3x8(y, inv);
-      if (byte == kScaleNan) q.x = q.y = kCodeNan4;
+      const uint2 q = e4m3x8(y, inv);
       *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.y) + at) = q;
       if ((threadIdx.x & 15) == 0) a.e[row * a.scale_cols + (c >> 4)] = static_cast<uint8_t>(byte);
     }
@@ -448,7 +447,7 @@ struct QuantArgs {
 // Largest magnitude of eight values, as float bits.
 __device__ __forceinline__ uint32_t amax8(const Vec8<__nv_bfloat16>& v) {
   constexpr uint32_t kM = 0x7FFF7FFFu;
-  const uint32_t m = __vmaxu2(__vmaxu2(v.q.x & kM, v.q.y & kM), __vmaxu2(v.q.z & kM, v.q.w & kM));
+  const uint32_t m = max_u16x2(max_u16x2(v.q.x & kM, v.q.y & kM), max_u16x2(v.q.z & kM, v.q.w & kM));
   return max(m & 0xFFFFu, m >> 16) << 16;
 }
 __device__ __forceinline__ uint32_t amax8(const Vec8<float>& v) {
@@ -480,12 +479,11 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_fp8_kernel(const Quant
   for (int u = 0; u < kQuantUnroll; ++u) {
     const uint32_t amax = block_max(amax8(x[u]));
     const uint32_t byte = scale_byte(amax);
-    const float inv = scale_inverse(byte == kScaleNan ? kScaleOne : byte);
+    const float inv = scale_inverse(byte);
     if (at[u] >= 0) {
       Pair f[4];
       x[u].get(f);
-      uint2 q = e4m3x8(f, inv);
-      if (byte == kScaleNan) q.x = q.y = kCodeNan4;
+      const uint2 q = e4m3x8(f, inv);
       *reinterpret_cast<uint2*>(a.y + at[u]) = q;
       if (t == 0) {   // the scale, and after a row's last block the row's padding
         const uint32_t b = b0 + u * kHalves, row = a.by_kb(b);
