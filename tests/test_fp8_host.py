@@ -7,6 +7,7 @@ import pytest
 import torch
 
 from oracle import sp24_oracle as O
+from structured_sparse_gemm_sp24_b200 import artifact as A
 from structured_sparse_gemm_sp24_b200 import build as sp24_build
 from structured_sparse_gemm_sp24_b200 import sp24 as B
 
@@ -122,6 +123,37 @@ def test_norm_backward_validation(lib):
     assert call(K=136) == B.SP24_ERR_ALIGN and call(dH=FAKE + 2) == B.SP24_ERR_ALIGN
     assert call(dgamma=FAKE + 4) == B.SP24_ERR_ALIGN and call(ws=FAKE + 8) == B.SP24_ERR_ALIGN
     assert call(K=B.SP24_NORM_MAX_K + 16) == B.SP24_ERR_UNSUPPORTED
+
+
+# ------------------------------------------------------ compressed-weight files
+def test_fp8_weight_file_round_trip(tmp_path, lib):
+    n, k = 130, 544
+    g = torch.Generator().manual_seed(1)
+    u8 = lambda *shape: torch.randint(0, 256, shape, dtype=torch.uint8, generator=g)  # noqa: E731
+    vals = u8(n, k // 2).view(torch.float8_e4m3fn)
+    meta = u8(B.sp24_meta_bytes(n, k))
+    e_w = u8(2, 8).view(torch.float8_e8m0fnu)
+    p = tmp_path / "w.sp24"
+    A.save_compressed(str(p), vals, meta, n, k, B.SP24_FP8, e_w)
+    assert p.stat().st_size == 64 + n * k // 2 + B.sp24_meta_bytes(n, k) + 16
+    w = A.load_compressed(str(p))
+    assert (w.n, w.k, w.dtype) == (n, k, B.SP24_FP8)
+    assert w.vals.dtype == torch.float8_e4m3fn and w.vals.shape == (n, k // 2)
+    assert w.s_w.dtype == torch.float8_e8m0fnu and w.s_w.shape == (2, 8)
+    assert torch.equal(w.vals.view(torch.uint8), vals.view(torch.uint8))
+    assert torch.equal(w.meta, meta)
+    assert torch.equal(w.s_w.view(torch.uint8), e_w.view(torch.uint8))
+    A.save_compressed(str(p), vals, meta, n, k, B.SP24_FP8, e_w.view(torch.uint8))   # bytes as well
+    assert torch.equal(A.load_compressed(str(p)).s_w.view(torch.uint8), e_w.view(torch.uint8))
+    with pytest.raises(ValueError):
+        A.save_compressed(str(p), vals, meta, n, k, B.SP24_FP8)                       # no scales
+    with pytest.raises(ValueError):
+        A.save_compressed(str(p), vals, meta, n, k, B.SP24_FP8, torch.ones(16))       # float scales
+    with pytest.raises(ValueError):
+        A.save_compressed(str(p), vals, meta, n, k, B.SP24_FP8, e_w[:1])
+    p.write_bytes(p.read_bytes()[:-1])
+    with pytest.raises(ValueError):
+        A.load_compressed(str(p))
 
 
 # ------------------------------------------------------------- oracle pins

@@ -253,6 +253,40 @@ def test_gemm_splits(m, n, k, split, monkeypatch):
     assert_product(out, y, a, k, False)
 
 
+@pytest.mark.parametrize("m", [9, 30, 60, 110])
+def test_gemm_more_row_tiles_than_sms(m):
+    """Several CTAs on an SM (the small ring), every token tile width; the sizes
+    are the plan's, so is the kernel."""
+    n, k = 19080, 1312                        # 150 row tiles
+    assert B.sp24_gemm_plan(m, n, k, B.SP24_FP8)["kernel"] == "splitk"
+    xq, e_x, vals, meta, e_w, y, a = product_case(m, n, k, m)
+    out = P.gemm_fp8(xq, e_x, vals, meta, e_w, n)
+    assert B.sp24_device_status() == B.SP24_OK
+    assert_product(out, y, a, k, True)
+
+
+def test_gemm_same_bits_again_and_back_to_back():
+    """Persistent tiles, many launches in a row: the same bits each time."""
+    m, n, k = 4096, 2304, 2048
+    w = P.prune_compress_fp8(rand((n, k), BF, 1, 0.02, 0.5).cuda())
+    xq, e_x = P.quantize_fp8(rand((m, k), F32, 2).cuda())
+    first = P.gemm_fp8(xq, e_x, *w, n)
+    outs = [P.gemm_fp8(xq, e_x, *w, n) for _ in range(40)]
+    assert B.sp24_device_status() == B.SP24_OK
+    assert all(torch.equal(first, o) for o in outs)
+
+
+def test_plan_uses_only_the_fp8_kernels(monkeypatch):
+    for m, n, k in [(1, 4096, 4096), (64, 11008, 4096), (2048, 11008, 4096), (8192, 4096, 4096),
+                    (300, 128, 512), (100000, 64, 256)]:
+        p = B.sp24_gemm_plan(m, n, k, B.SP24_FP8)
+        assert p["kernel"] in ("splitk", "pair256", "pair240", "pair224")
+        assert p["split_k"] in (1, 2, 4, 8)
+    for impl in ("single", "pair192", "pair128"):
+        monkeypatch.setenv("SP24_GEMM_IMPL", impl)
+        assert B.sp24_gemm_plan(4096, 4096, 4096, B.SP24_FP8)["kernel"].startswith("pair2")
+
+
 def test_gemm_of_exact_sums_is_exact():
     """Small whole numbers with power-of-two scales: every sum is exact in fp32,
     so any wrong scale, position or K range shows."""
@@ -540,6 +574,33 @@ def test_norm_feeds_the_int8_product():
     dy = torch.ones((m, n), device="cuda") @ wd
     dx, dg = P.rmsnorm_backward(dy.to(BF), o.h, gamma, o.rstd)
     assert_back(dx, dg, x.cpu(), gamma.cpu(), dy.to(BF).cpu(), None, o.rstd.cpu(), True)
+
+
+def test_norm_of_rows_with_an_exact_root():
+    """A row whose 1 / rms is a power of two: no remainder, so y is exact and ties
+    go to the even code; rows of equal magnitudes and both signs."""
+    k = 256
+    x = torch.ones((3, k))
+    x[0, ::2] = -1
+    x[1] = 0.25
+    x[2] = 0.25
+    gamma = torch.tensor([1.0, 1.0625, 1.1875, -1.3125] * (k // 4))   # e4m3 ties among them
+    o = P.rmsnorm_quant(x.cuda(), gamma.cuda(), eps=0.0, want_rstd=True)
+    y = torch.sign(x.double()) * gamma.double()
+    assert o.rstd.cpu().tolist() == [1.0, 4.0, 4.0]
+    want_q, want_e = O.fp8_rows(y.numpy())
+    assert_scales(o.e_y, want_e, k)
+    np.testing.assert_array_equal(f64(o.y), want_q)
+
+
+def test_norm_sum_of_subnormals_and_large_values():
+    """bf16 sums keep subnormals and round once."""
+    v = torch.tensor([1.0, 2.0 ** -8, 2.0 ** -9, 2.0 ** -130, 3 * 2.0 ** -133, 3e38, -0.0, 257.0])
+    x = v.repeat(32).to(BF).view(1, 256)
+    r = torch.tensor([2.0 ** -8, 1.0, 1.0, 2.0 ** -131, 2.0 ** -133, 1e36, -0.0, 0.5]).repeat(32)
+    r = r.to(BF).view(1, 256)
+    o = P.rmsnorm_quant(x.cuda(), torch.ones(256, dtype=BF, device="cuda"), r.cuda())
+    assert torch.equal(o.h.cpu().view(torch.int16), (x.float() + r.float()).to(BF).view(torch.int16))
 
 
 def test_two_streams_and_threads():
