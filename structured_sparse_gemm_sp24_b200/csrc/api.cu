@@ -143,7 +143,7 @@ const char* sp24_strerror(int status) {
   }
 }
 
-int sp24_version(void) { return 300; }
+int sp24_version(void) { return 400; }
 
 const char* sp24_last_cuda_error(void) { return g_last_err; }
 

@@ -170,9 +170,10 @@ def _ptr(t: Optional[torch.Tensor]):
     return t.data_ptr()
 
 
-def _stream(stream) -> Optional[int]:
+def _stream(stream, dev: Optional[int] = None) -> Optional[int]:
     if stream is None:   # (current_stream() builds a Python object: 3 us a call)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(
+            torch.cuda.current_device() if dev is None else dev)
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -391,7 +392,7 @@ def sp24_quantize_fp8(X: torch.Tensor, Xq: torch.Tensor, e_x: torch.Tensor, stre
     _check(lib().sp24_quantize_fp8(
         _arg(X, "X", _CODE_OF, n, dev), M, K, _CODE_OF.get(X.dtype, -1),
         _arg(Xq, "Xq", _FP8, n, dev), _arg(e_x, "e_x", _SCALE, M * _scale_cols(K), dev),
-        _stream(stream)), "sp24_quantize_fp8")
+        _stream(stream, dev)), "sp24_quantize_fp8")
 
 
 def sp24_prune_compress_fp8(W: torch.Tensor, mode: int, norms: Optional[torch.Tensor],
@@ -408,7 +409,7 @@ def sp24_prune_compress_fp8(W: torch.Tensor, mode: int, norms: Optional[torch.Te
         _arg(vals, "vals", _FP8, N * (K // 2), dev),
         _arg(meta, "meta", (torch.uint8,), _meta_numel(meta, N, K), dev),
         _arg(e_w, "e_w", _SCALE, (N + 127) // 128 * _scale_cols(K), dev),
-        _stream(stream)), "sp24_prune_compress_fp8")
+        _stream(stream, dev)), "sp24_prune_compress_fp8")
 
 
 def sp24_compress_fp8(W: torch.Tensor, mask: torch.Tensor, vals: torch.Tensor,
@@ -421,7 +422,7 @@ def sp24_compress_fp8(W: torch.Tensor, mask: torch.Tensor, vals: torch.Tensor,
         _arg(vals, "vals", _FP8, N * (K // 2), dev),
         _arg(meta, "meta", (torch.uint8,), _meta_numel(meta, N, K), dev),
         _arg(e_w, "e_w", _SCALE, (N + 127) // 128 * _scale_cols(K), dev),
-        _stream(stream)), "sp24_compress_fp8")
+        _stream(stream, dev)), "sp24_compress_fp8")
 
 
 def _meta_numel(meta: torch.Tensor, N: int, K: int) -> int:
@@ -441,7 +442,7 @@ def sp24_gemm_fp8(X: torch.Tensor, e_x: torch.Tensor, vals: torch.Tensor, meta: 
         _arg(vals, "vals", _FP8, N * (K // 2), dev),
         _arg(meta, "meta", (torch.uint8,), _meta_numel(meta, N, K), dev),
         _arg(e_w, "e_w", _SCALE, (N + 127) // 128 * _scale_cols(K), dev), N, out_kind,
-        _arg(Y, "Y", (ydt,), M * N, dev), _stream(stream)), "sp24_gemm_fp8")
+        _arg(Y, "Y", (ydt,), M * N, dev), _stream(stream, dev)), "sp24_gemm_fp8")
 
 
 _NORM_OUT = {SP24_FP8: _FP8, SP24_INT8: (torch.int8,), SP24_BF16: (torch.bfloat16,)}
@@ -460,7 +461,7 @@ def sp24_rmsnorm_quant(X: torch.Tensor, R: Optional[torch.Tensor], gamma: torch.
         _arg(s_x, "s_x", (torch.float32,), 1, dev), _arg(H, "H", dt, n, dev),
         _arg(Y, "Y", _NORM_OUT.get(out_dtype, ()), n, dev),
         _arg(e_y, "e_y", _SCALE, M * _scale_cols(K), dev),
-        _arg(rstd, "rstd", (torch.float32,), M, dev), _stream(stream)), "sp24_rmsnorm_quant")
+        _arg(rstd, "rstd", (torch.float32,), M, dev), _stream(stream, dev)), "sp24_rmsnorm_quant")
 
 
 def sp24_rmsnorm_backward(dY: torch.Tensor, dH: Optional[torch.Tensor], H: torch.Tensor,
@@ -475,7 +476,7 @@ def sp24_rmsnorm_backward(dY: torch.Tensor, dH: Optional[torch.Tensor], H: torch
         _CODE_OF.get(H.dtype, -1), _arg(dX, "dX", dt, n, dev),
         _arg(dgamma, "dgamma", (torch.float32,), K, dev),
         _arg(workspace, "workspace", (torch.uint8,), workspace.numel(), dev),
-        workspace.numel(), _stream(stream)), "sp24_rmsnorm_backward")
+        workspace.numel(), _stream(stream, dev)), "sp24_rmsnorm_backward")
 
 
 def sp24_selftest_wait_timeout(limit_ns: int, stream=None) -> None:

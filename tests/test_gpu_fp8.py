@@ -6,7 +6,7 @@ outputs equal the oracle's bit for bit.  Where arithmetic in fp32 comes first
 arithmetic's error of a rounding border.  Bounds:
 
 * norm output y: the row sum has at most 8 * NV + 5 + 32 <= 70 roundings of
-  positive terms, halved by the square root; mean, eps, the root and two
+  positive terms, halved by the square root; mean, eps, the root and the
   products add at most 6: 41 half-steps of 2^-24, taken as NORM_REL = 64 * 2^-24;
 * gemm: the fp32 sum takes K / 64 additions, each off by at most one unit
   2^-23 of a partial sum of at most sum |x w|, and as much again inside the
@@ -182,6 +182,20 @@ def test_convert_is_exact(n, k, masked, mode):
     assert torch.equal(meta2, meta)
     assert torch.equal(e2.view(torch.uint8), e.view(torch.uint8))
     assert B.sp24_device_status() == B.SP24_OK
+
+
+def test_convert_of_an_infinite_weight():
+    """The block of an infinity or NaN is NaN, its neighbours and mask are not."""
+    w = rand((256, 256), BF, 3, 0.02)
+    clean = P.prune_compress_fp8(w.cuda())
+    w[130, 7] = float("inf")
+    w[5, 200] = float("nan")
+    vals, meta, e = P.prune_compress_fp8(w.cuda())
+    by, q = e.view(torch.uint8).cpu(), vals.view(torch.uint8).cpu()
+    cq, cb = clean[0].view(torch.uint8).cpu(), clean[2].view(torch.uint8).cpu()
+    assert by[1, 0] == 255 and by[0, 1] == 255 and by[0, 0] == cb[0, 0] and by[1, 1] == cb[1, 1]
+    assert (q[128:, :64] == 0x7F).all() and (q[:128, 64:] == 0x7F).all()
+    assert torch.equal(q[:128, :64], cq[:128, :64]) and torch.equal(q[128:, 64:], cq[128:, 64:])
 
 
 def test_compress_reports_a_bad_group():
@@ -393,6 +407,31 @@ def test_norm_int8_and_bf16(m, k, dt):
     assert ((got == lo) | (got == hi)).all()
     o = P.rmsnorm_quant(x.cuda(), gamma.cuda(), r.cuda(), EPS, B.SP24_BF16)
     assert (np.abs(f64(o.y) - y) <= (HALF_BF16 + 2 * NORM_REL) * np.abs(y)).all()
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("m,k", [(297, 528), (296, 2048), (297, 2048), (297, 8192), (150, 12288),
+                                 (3, 12304), (149, 16384)])
+def test_norm_at_the_kernel_borders(m, k, dt):
+    """Row lengths and counts on both sides of every choice of kernel."""
+    x, r = rand((m, k), dt, m), rand((m, k), dt, k)
+    gamma = (1 + 0.2 * torch.randn(k, generator=torch.Generator().manual_seed(k))).to(dt)
+    o = P.rmsnorm_quant(x.cuda(), gamma.cuda(), r.cuda(), EPS, want_rstd=True)
+    h = stored_sum(x, r)
+    assert torch.equal(o.h.cpu(), h)
+    y, s = O.rmsnorm(f64(h), f64(gamma), EPS)
+    np.testing.assert_allclose(f64(o.rstd), s, rtol=NORM_REL)
+    assert_codes_near(o.y, o.e_y, y, NORM_REL, k)
+    dy = rand((m, k), dt, 3, 1.0, 0.5)
+    dx, dg = P.rmsnorm_backward(dy.cuda(), o.h, gamma.cuda(), o.rstd, dH=o.h)
+    assert_back(dx, dg, h, gamma, dy, h, o.rstd.cpu(), dt is BF)
+
+
+def test_norm_copies_the_stream_without_a_residual():
+    x = rand((5, 528), BF, 1).cuda()
+    h = torch.zeros_like(x)
+    o = P.rmsnorm_quant(x, torch.ones(528, dtype=BF, device="cuda"), out_sum=h)
+    assert o.h is h and torch.equal(h, x)
 
 
 def test_norm_in_place_stream_and_zero_rows():
