@@ -244,7 +244,8 @@ sp24_status make_plan(int64_t m, int64_t n, int kblocks, int dtype, Plan* p) {
   // The split.  With the issue loop that built every descriptor anew a stage took
   // the issuing thread about the same time whatever the token count (measured on
   // B200: ~0.44 us per 128-channel x 128-K stage at 16 tokens, ~0.5 us at 256), so
-  // at few tokens the kernel was bound by the stages the busiest SM runs: ceil(CTAs / SMs) x stages per CTA.  The plan
+  // at few tokens the kernel was bound by the stages the busiest SM runs:
+  // ceil(CTAs / SMs) x stages per CTA.  The plan
   // takes the split among 1, 2, 4, 8 (at least 4 stages per CTA) that
   // minimises it, the fewer CTAs on a tie; more than one CTA per SM takes
   // the small ring.  E.g. M = 16, 11008 x 4096 (86 row tiles, 32 stages):

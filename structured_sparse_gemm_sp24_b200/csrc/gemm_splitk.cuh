@@ -212,7 +212,8 @@ gemm_sp_kernel(const __grid_constant__ CUtensorMap tmap_a,
         if (lane == 0) ok = mbar_wait(&empty_bar[s], ((i / STAGES) & 1u) ^ 1u);
         if (!__shfl_sync(0xffffffffu, ok, 0)) { *abort_flag = 1; break; }
         if (sf_load_stage(kb, kb_begin)) {
-          words.store(smem + STAGES * C::kStageStride + (sf_n % C::kSfBufs) * C::Sf::kSmemBuf, 0, lane);
+          words.store(smem + STAGES * C::kStageStride + (sf_n % C::kSfBufs) * C::Sf::kSmemBuf, 0,
+                      lane);
           ++sf_n;
           const int next = kb / 2 + 1;
           if (2 * next < kb_end)

@@ -655,7 +655,7 @@ __global__ void __launch_bounds__(512) norm_back_kernel(const BackArgs a, int gr
 
 // The same for rows too long for the registers: one row a block at a time, the
 // rows in `slots` slots of dy, h (and dh) in shared memory, filled by bulk copies
-// that run ahead (2000 x 11008 with dh: 38.4 us; four vectors a thread in
+// that run ahead (2000 x 11008 with dh: 37.5 us; four vectors a thread in
 // registers 72.7.  8192 x 4096: 49.7 against 50.4; 8192 x 768: 18.2 against 15.1).
 // A slot is read in both passes over its row; it is refilled after the next
 // row's sum, whose barrier says that the block has left it.
