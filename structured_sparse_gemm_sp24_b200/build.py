@@ -1,16 +1,20 @@
-"""Builds libsp24.so (the C-ABI library) in-tree with nvcc for sm_100a."""
+"""Builds libsp24.so (the C-ABI library) in-tree with nvcc for sm_100a, and
+_binding.so (the native half of the Python binding) with g++."""
 from __future__ import annotations
 
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libsp24.so")
+BINDING = os.path.join(HERE, "_binding.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -43,19 +47,47 @@ def needs_build() -> bool:
     return any(os.path.getmtime(s) > t for s in _sources())
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile libsp24.so unless it is up to date; returns its path."""
-    if not force and not needs_build():
-        return LIB
-    tmp = LIB + ".tmp"
-    cmd = [nvcc_path(), *NVCC_FLAGS, "-I", INCLUDE, os.path.join(CSRC, "libsp24.cu"), "-o", tmp]
+def _run(cmd, verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
-        raise RuntimeError(f"nvcc failed ({res.returncode}):\n{res.stdout}\n{res.stderr}")
+        raise RuntimeError(f"{cmd[0]} failed ({res.returncode}):\n{res.stdout}\n{res.stderr}")
     if verbose and (res.stdout or res.stderr):
         print(res.stdout, res.stderr, file=sys.stderr)
+
+
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    """Compile _binding.so (against torch's headers) unless it is up to date."""
+    deps = [BINDING_SRC, os.path.join(INCLUDE, "sp24.h")]
+    if not force and os.path.exists(BINDING) and all(
+            os.path.getmtime(d) <= os.path.getmtime(BINDING) for d in deps):
+        return BINDING
+    import torch
+    t = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path())))
+    lib = os.path.join(t, "lib")
+    tmp = BINDING + ".tmp"
+    _run(["g++", "-O2", "-std=c++17", "-shared", "-fPIC",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          "-I", sysconfig.get_paths()["include"], "-I", os.path.join(t, "include"),
+          "-I", os.path.join(t, "include", "torch", "csrc", "api", "include"),
+          "-I", os.path.join(cuda, "include"), BINDING_SRC, "-o", tmp,
+          "-L", lib, f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"],
+         verbose)
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """Compile libsp24.so and _binding.so unless they are up to date; returns the
+    library's path."""
+    build_binding(force, verbose)
+    if not force and not needs_build():
+        return LIB
+    tmp = LIB + ".tmp"
+    cmd = [nvcc_path(), *NVCC_FLAGS, "-I", INCLUDE, os.path.join(CSRC, "libsp24.cu"), "-o", tmp]
+    _run(cmd, verbose)
     os.replace(tmp, LIB)
     return LIB
 

@@ -125,8 +125,12 @@ def gemm(X: torch.Tensor, vals: torch.Tensor, meta: torch.Tensor, N: int,
     return out
 
 
+# type codes of the native allocation (half the time of Tensor.new_empty)
+_SAME, _I8, _BF16, _F32, _E4M3, _E8M0, _U8 = range(7)
+
+
 def _scales(rows: int, K: int, like: torch.Tensor) -> torch.Tensor:
-    return like.new_empty((rows, 4 * ((K + 511) // 512)), dtype=torch.float8_e8m0fnu)
+    return _b.native().new_empty(like, _E8M0, rows, 4 * ((K + 511) // 512))
 
 
 def quantize_fp8(X: torch.Tensor, out: Optional[torch.Tensor] = None,
@@ -135,7 +139,7 @@ def quantize_fp8(X: torch.Tensor, out: Optional[torch.Tensor] = None,
     blocks of 128 columns [M, 4 * ceil(K / 512)] (columns past the last block: 1)."""
     M, K = X.shape
     if out is None:
-        out = X.new_empty((M, K), dtype=torch.float8_e4m3fn)
+        out = _b.native().new_empty(X, _E4M3, M, K)
     if out_scales is None:
         out_scales = _scales(M, K, X)
     _b.sp24_quantize_fp8(X, out, out_scales)
@@ -143,8 +147,8 @@ def quantize_fp8(X: torch.Tensor, out: Optional[torch.Tensor] = None,
 
 
 def _alloc_fp8_weight(N: int, K: int, like: torch.Tensor):
-    return (like.new_empty((N, K // 2), dtype=torch.float8_e4m3fn),
-            like.new_empty(_b.sp24_meta_bytes(N, K), dtype=torch.uint8),
+    new = _b.native().new_empty
+    return (new(like, _E4M3, N, K // 2), _b.native().new_meta(like, N, K),
             _scales((N + 127) // 128, K, like))
 
 
@@ -155,7 +159,7 @@ def prune_compress_fp8(W: torch.Tensor, mode: int = _b.SP24_MAGNITUDE,
     with one e8m0 scale per 128 x 128 block."""
     N, K = W.shape
     vals, meta, e_w = _alloc_fp8_weight(N, K, W)
-    mask = W.new_empty((N, K // 8), dtype=torch.uint8) if want_mask else None
+    mask = _b.native().new_empty(W, _U8, N, K // 8) if want_mask else None
     _b.sp24_prune_compress_fp8(W, mode, norms, mask_in, mask, vals, meta, e_w)
     return (vals, meta, e_w, mask) if want_mask else (vals, meta, e_w)
 
@@ -174,8 +178,7 @@ def gemm_fp8(X: torch.Tensor, e_x: torch.Tensor, vals: torch.Tensor, meta: torch
     """Y [M, N] = X W'^T of e4m3 activations (X, e_x) and a converted weight
     (vals, meta, e_w); bf16 or (SP24_OUT_F32) float32."""
     if out is None:
-        odt = torch.float32 if out_kind == _b.SP24_OUT_F32 else torch.bfloat16
-        out = X.new_empty((X.shape[0], N), dtype=odt)
+        out = _b.native().new_empty(X, _F32 if out_kind == _b.SP24_OUT_F32 else _BF16, X.shape[0], N)
     _b.sp24_gemm_fp8(X, e_x, vals, meta, e_w, N, out_kind, out)
     return out
 
@@ -187,8 +190,7 @@ class RmsNorm(NamedTuple):
     rstd: Optional[torch.Tensor]     # float32 [M] when asked for
 
 
-_NORM_TORCH = {_b.SP24_FP8: torch.float8_e4m3fn, _b.SP24_INT8: torch.int8,
-               _b.SP24_BF16: torch.bfloat16}
+_NORM_TYPE = {_b.SP24_FP8: _E4M3, _b.SP24_INT8: _I8, _b.SP24_BF16: _BF16}
 
 
 def rmsnorm_quant(X: torch.Tensor, gamma: torch.Tensor, residual: Optional[torch.Tensor] = None,
@@ -201,14 +203,14 @@ def rmsnorm_quant(X: torch.Tensor, gamma: torch.Tensor, residual: Optional[torch
     gemm) or bf16.  out_sum may be X or residual: the stream updated in place."""
     M, K = X.shape
     if out is None:
-        out = X.new_empty((M, K), dtype=_NORM_TORCH[out_dtype])
+        out = _b.native().new_empty(X, _NORM_TYPE[out_dtype], M, K)
     if out_dtype != _b.SP24_FP8:
         out_scales = None
     elif out_scales is None:
         out_scales = _scales(M, K, X)
     if out_sum is None and residual is not None:
-        out_sum = torch.empty_like(X)
-    rstd = X.new_empty(M, dtype=torch.float32) if want_rstd else None
+        out_sum = _b.native().new_empty(X, _SAME, M, K)
+    rstd = _b.native().new_empty(X, _F32, M) if want_rstd else None
     _b.sp24_rmsnorm_quant(X, residual, gamma, eps, out_dtype, s_x, out_sum, out, out_scales, rstd)
     return RmsNorm(out, out_scales, X if out_sum is None else out_sum, rstd)
 
@@ -221,10 +223,10 @@ def rmsnorm_backward(dY: torch.Tensor, H: torch.Tensor, gamma: torch.Tensor, rst
     dH is the gradient that reaches H past the norm."""
     M, K = H.shape
     if out is None:
-        out = torch.empty_like(H)
+        out = _b.native().new_empty(H, _SAME, M, K)
     if workspace is None:
-        workspace = H.new_empty(_b.sp24_rmsnorm_backward_workspace_bytes(M, K), dtype=torch.uint8)
-    dgamma = H.new_empty(K, dtype=torch.float32)
+        workspace = _b.native().new_workspace(H, M, K)
+    dgamma = _b.native().new_empty(H, _F32, K)
     _b.sp24_rmsnorm_backward(dY, dH, H, gamma, rstd, out, dgamma, workspace)
     return out, dgamma
 

@@ -3,7 +3,9 @@
 Argument marshalling only: every function takes torch tensors that already
 live on the device, checks that they are dense and on CUDA, and passes their
 pointers, sizes and the current CUDA stream to the C function of the same
-name.  All computation happens in the library's CUDA kernels; there is no
+name.  The e4m3 and norm functions, which matter at single tokens, are checked
+and called by a native module (csrc/binding.cpp, _binding.so); it also checks
+types, sizes and the device.  All computation happens in the library's CUDA kernels; there is no
 fallback path.  A non-OK status raises :class:`Sp24Error`.
 """
 from __future__ import annotations
@@ -151,6 +153,34 @@ def lib() -> ctypes.CDLL:
     return _LIB
 
 
+_NATIVE = None
+_NATIVE_FUNCTIONS = ("sp24_quantize_fp8", "sp24_prune_compress_fp8", "sp24_compress_fp8",
+                     "sp24_gemm_fp8", "sp24_rmsnorm_quant", "sp24_rmsnorm_backward",
+                     "sp24_meta_bytes", "sp24_rmsnorm_backward_workspace_bytes")
+
+
+def native():
+    """The native half of the binding, bound to the loaded library.  Raises if
+    _binding.so has not been built."""
+    global _NATIVE
+    if _NATIVE is None:
+        h = lib()
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise RuntimeError(
+                "_binding.so is missing or does not load: build it with "
+                "`python -m structured_sparse_gemm_sp24_b200.build`") from e
+        _binding.bind(*(ctypes.cast(getattr(h, f), _c_p).value for f in _NATIVE_FUNCTIONS))
+        _NATIVE = _binding
+    return _NATIVE
+
+
+def _raw(stream) -> Optional[int]:
+    """A raw stream for the native functions (None: torch's current stream)."""
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else stream
+
+
 def strerror(status: int) -> str:
     return lib().sp24_strerror(int(status)).decode()
 
@@ -170,45 +200,12 @@ def _ptr(t: Optional[torch.Tensor]):
     return t.data_ptr()
 
 
-def _stream(stream, dev: Optional[int] = None) -> Optional[int]:
+def _stream(stream) -> Optional[int]:
     if stream is None:   # (current_stream() builds a Python object: 3 us a call)
-        return torch._C._cuda_getCurrentRawStream(
-            torch.cuda.current_device() if dev is None else dev)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
-
-
-# Element types of the e4m3 and norm entry points (whose tensors are checked:
-# a wrong type or size would be read as another).
-_CODE_OF = {torch.bfloat16: SP24_BF16, torch.float32: SP24_F32}
-_FP8 = (torch.float8_e4m3fn,)
-_SCALE = (torch.float8_e8m0fnu, torch.uint8)
-
-
-def _arg(t: Optional[torch.Tensor], name: str, dtypes, numel: int, dev: int):
-    """Pointer of a dense CUDA tensor of one of `dtypes` with `numel` elements on
-    device `dev`; None stays None."""
-    if t is None:
-        return None
-    if (t.get_device() != dev or t.dtype not in dtypes or t.numel() != numel
-            or not t.is_contiguous()):
-        if t.get_device() != dev:
-            raise ValueError(f"sp24: {name} must be a CUDA tensor on the current device ({dev})")
-        if t.dtype not in dtypes:
-            raise ValueError(f"sp24: {name} has type {t.dtype}, expected one of {tuple(dtypes)}")
-        raise ValueError(f"sp24: {name} must be contiguous with {numel} elements")
-    return t.data_ptr()
-
-
-def _matrix(t: torch.Tensor, name: str):
-    if t.dim() != 2:
-        raise ValueError(f"sp24: {name} must be a matrix, got {tuple(t.shape)}")
-    return t.shape
-
-
-def _scale_cols(K: int) -> int:
-    return 4 * ((K + 511) // 512)
 
 
 # ------------------------------------------------------------------- sizes
@@ -387,65 +384,29 @@ def sp24_im2col3x3(X: torch.Tensor, A: torch.Tensor, stream=None) -> None:
 
 def sp24_quantize_fp8(X: torch.Tensor, Xq: torch.Tensor, e_x: torch.Tensor, stream=None) -> None:
     """X bf16 or float32 [M, K] -> e4m3 codes [M, K] and e8m0 scales."""
-    M, K = _matrix(X, "X")
-    dev, n = torch.cuda.current_device(), X.numel()
-    _check(lib().sp24_quantize_fp8(
-        _arg(X, "X", _CODE_OF, n, dev), M, K, _CODE_OF.get(X.dtype, -1),
-        _arg(Xq, "Xq", _FP8, n, dev), _arg(e_x, "e_x", _SCALE, M * _scale_cols(K), dev),
-        _stream(stream, dev)), "sp24_quantize_fp8")
+    _check(native().quantize_fp8(X, Xq, e_x, _raw(stream)), "sp24_quantize_fp8")
 
 
 def sp24_prune_compress_fp8(W: torch.Tensor, mode: int, norms: Optional[torch.Tensor],
                             mask_in: Optional[torch.Tensor], mask_out: Optional[torch.Tensor],
                             vals: torch.Tensor, meta: torch.Tensor, e_w: torch.Tensor,
                             stream=None) -> None:
-    N, K = _matrix(W, "W")
-    dev, mb = torch.cuda.current_device(), N * (K // 8)
-    _check(lib().sp24_prune_compress_fp8(
-        _arg(W, "W", (torch.bfloat16,), N * K, dev), N, K, mode,
-        _arg(norms, "norms", (torch.float64,), K, dev),
-        _arg(mask_in, "mask_in", (torch.uint8,), mb, dev),
-        _arg(mask_out, "mask_out", (torch.uint8,), mb, dev),
-        _arg(vals, "vals", _FP8, N * (K // 2), dev),
-        _arg(meta, "meta", (torch.uint8,), _meta_numel(meta, N, K), dev),
-        _arg(e_w, "e_w", _SCALE, (N + 127) // 128 * _scale_cols(K), dev),
-        _stream(stream, dev)), "sp24_prune_compress_fp8")
+    """e4m3 weight conversion of bf16 W [N, K] in one pass."""
+    _check(native().prune_compress_fp8(W, mode, norms, mask_in, mask_out, vals, meta, e_w,
+                                       _raw(stream)), "sp24_prune_compress_fp8")
 
 
 def sp24_compress_fp8(W: torch.Tensor, mask: torch.Tensor, vals: torch.Tensor,
                       meta: torch.Tensor, e_w: torch.Tensor, stream=None) -> None:
-    N, K = _matrix(W, "W")
-    dev = torch.cuda.current_device()
-    _check(lib().sp24_compress_fp8(
-        _arg(W, "W", (torch.bfloat16,), N * K, dev),
-        _arg(mask, "mask", (torch.uint8,), N * (K // 8), dev), N, K,
-        _arg(vals, "vals", _FP8, N * (K // 2), dev),
-        _arg(meta, "meta", (torch.uint8,), _meta_numel(meta, N, K), dev),
-        _arg(e_w, "e_w", _SCALE, (N + 127) // 128 * _scale_cols(K), dev),
-        _stream(stream, dev)), "sp24_compress_fp8")
-
-
-def _meta_numel(meta: torch.Tensor, N: int, K: int) -> int:
-    """Elements expected of a metadata tensor: at least the layout's bytes (an
-    allocation may be larger)."""
-    return max((N + 127) // 128 * ((K + 127) // 128) * 2048, meta.numel())
+    """The same conversion under a given mask."""
+    _check(native().compress_fp8(W, mask, vals, meta, e_w, _raw(stream)), "sp24_compress_fp8")
 
 
 def sp24_gemm_fp8(X: torch.Tensor, e_x: torch.Tensor, vals: torch.Tensor, meta: torch.Tensor,
                   e_w: torch.Tensor, N: int, out_kind: int, Y: torch.Tensor, stream=None) -> None:
     """Y [M, N] = X W'^T of e4m3 X [M, K] and a compressed e4m3 weight."""
-    M, K = _matrix(X, "X")
-    dev = torch.cuda.current_device()
-    ydt = torch.float32 if out_kind == SP24_OUT_F32 else torch.bfloat16
-    _check(lib().sp24_gemm_fp8(
-        _arg(X, "X", _FP8, M * K, dev), _arg(e_x, "e_x", _SCALE, M * _scale_cols(K), dev), M, K,
-        _arg(vals, "vals", _FP8, N * (K // 2), dev),
-        _arg(meta, "meta", (torch.uint8,), _meta_numel(meta, N, K), dev),
-        _arg(e_w, "e_w", _SCALE, (N + 127) // 128 * _scale_cols(K), dev), N, out_kind,
-        _arg(Y, "Y", (ydt,), M * N, dev), _stream(stream, dev)), "sp24_gemm_fp8")
-
-
-_NORM_OUT = {SP24_FP8: _FP8, SP24_INT8: (torch.int8,), SP24_BF16: (torch.bfloat16,)}
+    _check(native().gemm_fp8(X, e_x, vals, meta, e_w, N, out_kind, Y, _raw(stream)),
+           "sp24_gemm_fp8")
 
 
 def sp24_rmsnorm_quant(X: torch.Tensor, R: Optional[torch.Tensor], gamma: torch.Tensor, eps: float,
@@ -453,30 +414,16 @@ def sp24_rmsnorm_quant(X: torch.Tensor, R: Optional[torch.Tensor], gamma: torch.
                        Y: torch.Tensor, e_y: Optional[torch.Tensor],
                        rstd: Optional[torch.Tensor], stream=None) -> None:
     """RMS norm of X (+ R) with an e4m3, int8 or bf16 output."""
-    M, K = _matrix(X, "X")
-    dev, n, dt = torch.cuda.current_device(), X.numel(), (X.dtype,)
-    _check(lib().sp24_rmsnorm_quant(
-        _arg(X, "X", _CODE_OF, n, dev), _arg(R, "R", dt, n, dev), _arg(gamma, "gamma", dt, K, dev),
-        M, K, _CODE_OF.get(X.dtype, -1), eps, out_dtype,
-        _arg(s_x, "s_x", (torch.float32,), 1, dev), _arg(H, "H", dt, n, dev),
-        _arg(Y, "Y", _NORM_OUT.get(out_dtype, ()), n, dev),
-        _arg(e_y, "e_y", _SCALE, M * _scale_cols(K), dev),
-        _arg(rstd, "rstd", (torch.float32,), M, dev), _stream(stream, dev)), "sp24_rmsnorm_quant")
+    _check(native().rmsnorm_quant(X, R, gamma, eps, out_dtype, s_x, H, Y, e_y, rstd, _raw(stream)),
+           "sp24_rmsnorm_quant")
 
 
 def sp24_rmsnorm_backward(dY: torch.Tensor, dH: Optional[torch.Tensor], H: torch.Tensor,
                           gamma: torch.Tensor, rstd: torch.Tensor, dX: torch.Tensor,
                           dgamma: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
     """Gradients of sp24_rmsnorm_quant to X (and R) and gamma."""
-    M, K = _matrix(H, "H")
-    dev, n, dt = torch.cuda.current_device(), H.numel(), (H.dtype,)
-    _check(lib().sp24_rmsnorm_backward(
-        _arg(dY, "dY", dt, n, dev), _arg(dH, "dH", dt, n, dev), _arg(H, "H", _CODE_OF, n, dev),
-        _arg(gamma, "gamma", dt, K, dev), _arg(rstd, "rstd", (torch.float32,), M, dev), M, K,
-        _CODE_OF.get(H.dtype, -1), _arg(dX, "dX", dt, n, dev),
-        _arg(dgamma, "dgamma", (torch.float32,), K, dev),
-        _arg(workspace, "workspace", (torch.uint8,), workspace.numel(), dev),
-        workspace.numel(), _stream(stream, dev)), "sp24_rmsnorm_backward")
+    _check(native().rmsnorm_backward(dY, dH, H, gamma, rstd, dX, dgamma, workspace, _raw(stream)),
+           "sp24_rmsnorm_backward")
 
 
 def sp24_selftest_wait_timeout(limit_ns: int, stream=None) -> None:

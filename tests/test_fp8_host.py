@@ -202,3 +202,45 @@ def test_fp8_gemm_and_norm_oracles_by_brute_force():
     p[2] += 1e-6
     q[2] -= 1e-6
     assert abs(((O.rmsnorm(h, p, 0.5)[0] - O.rmsnorm(h, q, 0.5)[0]) * dy).sum() / 2e-6 - dg[2]) < 1e-8
+
+
+def test_binding_refuses_before_any_cuda_call(lib):
+    n = B.native()
+    cpu = torch.zeros(4, 128)
+    with pytest.raises(ValueError, match="X must be a CUDA tensor"):
+        n.quantize_fp8(cpu, cpu, cpu, None)
+    with pytest.raises(ValueError, match="X must be a matrix"):
+        n.quantize_fp8(torch.zeros(4), cpu, cpu, None)
+    with pytest.raises(ValueError, match="H must be a tensor"):
+        n.rmsnorm_backward(cpu, None, None, cpu, cpu, cpu, cpu, cpu, None)
+    with pytest.raises(ValueError, match="W must be a CUDA tensor"):
+        B.sp24_prune_compress_fp8(cpu, B.SP24_MAGNITUDE, None, None, None, cpu, cpu, cpu)
+    with pytest.raises(ValueError, match="unknown type code"):
+        n.new_empty(cpu, 7, 1)
+    with pytest.raises(RuntimeError, match="wrong number of arguments"):
+        n.gemm_fp8(cpu)
+    with pytest.raises(TypeError):
+        n.new_empty(cpu, 1, 2.5)
+
+
+def test_binding_allocations(lib):
+    n = B.native()
+    like = torch.zeros(2, 3, dtype=torch.bfloat16, requires_grad=True)
+    types = [torch.bfloat16, torch.int8, torch.bfloat16, torch.float32, torch.float8_e4m3fn,
+             torch.float8_e8m0fnu, torch.uint8]
+    for code, t in enumerate(types):
+        e = n.new_empty(like, code, 3, 5)
+        assert e.dtype == t and e.shape == (3, 5) and e.is_contiguous() and not e.requires_grad
+    assert n.new_empty(like, 3, 0).shape == (0,)
+    assert n.new_meta(like, 65, 192).numel() == B.sp24_meta_bytes(65, 192)
+    assert n.new_workspace(like, 7, 4096).numel() == B.sp24_rmsnorm_backward_workspace_bytes(7, 4096)
+
+
+def test_binding_missing_is_an_error(lib, monkeypatch):
+    import sys
+    import structured_sparse_gemm_sp24_b200 as pkg
+    monkeypatch.setattr(B, "_NATIVE", None)
+    monkeypatch.setitem(sys.modules, pkg.__name__ + "._binding", None)
+    monkeypatch.delattr(pkg, "_binding", raising=False)
+    with pytest.raises(RuntimeError, match="_binding.so"):
+        B.native()
