@@ -431,7 +431,9 @@ sp24_status sp24_gemm_fp8(const void* X, const uint8_t* e_x, int64_t M, int64_t 
  *   rstd: float32 [M], receives s for sp24_rmsnorm_backward (nullable).
  * Rules: M >= 0, 1 <= K <= SP24_NORM_MAX_K, K % 16 == 0, eps >= 0; e_y required
  * for SP24_FP8, s_x (one float32, device) for SP24_INT8; pointers 16-byte
- * aligned (rstd and s_x: 4).  A row of zeros gives zeros when eps > 0. */
+ * aligned (rstd and s_x: 4).  A row of zeros gives zeros when eps > 0.  A y that
+ * overflows fp32 (or, for SP24_FP8, comes within 2^-23 of its largest number)
+ * counts as an infinity. */
 sp24_status sp24_rmsnorm_quant(const void* X, const void* R, const void* gamma, int64_t M,
                                int64_t K, int x_dtype, float eps, int out_dtype, const float* s_x,
                                void* H, void* Y, uint8_t* e_y, float* rstd, void* stream);

@@ -302,7 +302,8 @@ __device__ __forceinline__ void norm_out(const NormArgs& a, const Vec8<T>& h, co
   if constexpr (OUT == SP24_FP8) {
     // (a NaN statistic makes NaNs of the zeros past the row)
     uint32_t amax = block_max(ok ? amax8(f) : 0u);
-    if (amax == 1u) amax = 0u;   // a block of zeros, rounded to odd
+    if (amax == 1u) amax = 0u;            // a block of zeros, rounded to odd
+    if (amax == 0x7F7FFFFFu) amax += 1u;  // truncation holds an overflow at the largest float
     const uint32_t byte = scale_byte(amax);
     const float inv = scale_inverse(byte);
     if (ok) {
@@ -829,7 +830,9 @@ __global__ void __launch_bounds__(256) dgamma_kernel(const float* part, int p, i
 
 // -------------------------------------------------------------- launching
 // Resident blocks per SM of a kernel at `threads` threads, asked once per
-// device and block size.
+// device and block size (the gradient's groups take at most 64 bytes of shared
+// memory a thread, 128 KB of a full SM, so its size never decides the answer and
+// the grid depends on the sizes of the call alone).
 struct Occupancy {
   std::atomic<int> per_sm[64][33];   // zero-initialised (static storage)
 };
@@ -909,7 +912,6 @@ static sp24_status launch_back_t(const BackArgs& a, int group_threads, float* dg
   // fewer where the rows are few
   int64_t groups = 512 / group_threads;
   if (groups > 15) groups = 15;
-
   const int64_t spread = (a.m + sm_count() - 1) / sm_count();
   if (groups > spread) groups = spread < 1 ? 1 : spread;
   const int threads = static_cast<int>(groups) * group_threads;

@@ -716,3 +716,24 @@ def test_binding_refuses_wrong_tensors():
         P.gemm_fp8(xq, e_x, vals, meta, e_w, 64, out_kind=B.SP24_OUT_INT8)
     assert e.value.status == B.SP24_ERR_ARG
     assert B.sp24_device_status() == B.SP24_OK
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_norm_of_an_overflowing_product(dt):
+    """|y| past the largest float32 makes its block NaN, as an infinity does; y just
+    below it stays finite."""
+    k = 256
+    x = torch.full((3, k), 2.0 ** -10, dtype=dt)
+    x[:, 0] = 2.0 ** -6                         # y / gamma = 2^-6 s, of order 10
+    gamma = torch.ones(k, dtype=dt)
+    gamma[0] = 2.0 ** 126                       # y of 1e39: above 3.4e38
+    q = P.rmsnorm_quant(x.cuda(), gamma.cuda(), eps=0.0)
+    s = 1.0 / np.sqrt((f64(x) ** 2).mean(axis=1))
+    assert (2.0 ** -6 * s * 2.0 ** 126 > 2.0 ** 128).all()
+    assert (q.e_y.view(torch.uint8)[:, 0] == 255).all() and (q.y.view(torch.uint8)[:, :128] == 0x7F).all()
+    assert (exps(q.e_y)[:, 1] < 10).all() and torch.isfinite(q.y[:, 128:].float()).all()
+    gamma[0] = 2.0 ** 123                       # y of 1e38
+    q = P.rmsnorm_quant(x.cuda(), gamma.cuda(), eps=0.0)
+    want = 2.0 ** -6 * s * 2.0 ** 123
+    got = f64(q.y)[:, 0] * 2.0 ** exps(q.e_y)[:, 0]
+    assert (np.abs(got - want) <= want * (2.0 ** -4 + NORM_REL)).all()
