@@ -737,3 +737,21 @@ def test_norm_of_an_overflowing_product(dt):
     want = 2.0 ** -6 * s * 2.0 ** 123
     got = f64(q.y)[:, 0] * 2.0 ** exps(q.e_y)[:, 0]
     assert (np.abs(got - want) <= want * (2.0 ** -4 + NORM_REL)).all()
+
+
+@pytest.mark.parametrize("m", [4, 600])
+@pytest.mark.parametrize("ex,ew", [(227, 27), (27, 227), (254, 3), (1, 254), (60, 68), (190, 60)])
+def test_gemm_scales_far_apart(m, ex, ew):
+    """Scales whose product is in range though neither is near one: exact (2^-126
+    and 2^127 among them, and sums at the edge of float32's normal range)."""
+    n, k = 256, 256
+    g = torch.Generator().manual_seed(1)
+    x = torch.randint(-3, 4, (m, k), generator=g).float().to(torch.float8_e4m3fn).cuda()
+    w = torch.randint(-3, 4, (n, k), generator=g).float().to(BF).cuda()
+    vals, meta, e_w = P.compress_fp8(w, P.prune(w))
+    full = lambda rows, v: torch.full((rows, 4), v, dtype=torch.uint8, device="cuda")
+    one = P.gemm_fp8(x, full(m, 127), vals, meta, full(2, 127), n, B.SP24_OUT_F32)
+    y = P.gemm_fp8(x, full(m, ex), vals, meta, full(2, ew), n, B.SP24_OUT_F32)
+    assert B.sp24_device_status() == B.SP24_OK
+    # the codes are whole multiples of 2^6 (three times 2^7 and below: 3 * 2^7 <= 448)
+    np.testing.assert_array_equal(f64(y), f64(one) * 2.0 ** (ex - 127 + ew - 127))
