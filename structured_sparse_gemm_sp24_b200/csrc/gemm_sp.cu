@@ -239,8 +239,8 @@ sp24_status make_plan(int64_t m, int64_t n, int kblocks, int dtype, Plan* p) {
     }
     return SP24_OK;
   }
-  const int bn = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128;
-  const int64_t base = row_tiles * ((m + bn - 1) / bn);
+  int bn = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128;
+  int64_t base = row_tiles * ((m + bn - 1) / bn);
   // The split.  With the issue loop that built every descriptor anew a stage took
   // the issuing thread about the same time whatever the token count (measured on
   // B200: ~0.44 us per 128-channel x 128-K stage at 16 tokens, ~0.5 us at 256), so
@@ -261,14 +261,34 @@ sp24_status make_plan(int64_t m, int64_t n, int kblocks, int dtype, Plan* p) {
   // e4m3 (with the lean issue loop): the largest split that keeps one CTA per
   // SM; sharing an SM costs more than it spreads (11008 x 4096: M = 1 8.25 us
   // with split 1 on 86 CTAs, 8.17 with 4; M = 16 8.3 and 8.7; M = 64 9.3 and 11.6;
-  // 4096 x 4096, M = 1: split 1 6.6, 4 4.8, 8 5.0).
-  for (int sp = 1; sp <= 8; sp *= 2) {
-    if (sp > 1 && kblocks < 4 * sp) break;
-    if (fp8) {
-      if (sp > 1 && base * sp > sms) break;
-      split = sp;
-      continue;
+  // 4096 x 4096, M = 1: split 1 6.6, 4 4.8, 8 5.0).  Above 64 tokens a stage takes
+  // the time of its rows' way into the SM (128 of weights, two halves of bn), so
+  // 96-token tiles are taken where they make the busiest SM load fewer: M = 333
+  // x 4104 x 4128 10.3 us on 132 CTAs, 11.9 with 128 tokens on 99; M = 80 x 4096 x
+  // 4096 6.9 and 7.6; M = 192 x 8192 x 4096 8.2 and 8.8; M = 288 x 5376 x 11008
+  // 15.6 and 16.7.
+  const auto one_per_sm = [&](int64_t tiles) {
+    int sp = 1;
+    while (sp < 8 && kblocks >= 8 * sp && tiles * 2 * sp <= sms) sp *= 2;
+    return sp;
+  };
+  if (fp8) {
+    split = one_per_sm(base);
+    if (bn == 128) {
+      const int64_t base96 = row_tiles * ((m + 95) / 96);
+      const int split96 = one_per_sm(base96);
+      const auto rows = [&](int tokens, int sp) {
+        return static_cast<int64_t>((kblocks + sp - 1) / sp) * (128 + 2 * tokens);
+      };
+      if (base96 <= sms && rows(96, split96) < rows(128, split)) {
+        bn = 96;
+        base = base96;
+        split = split96;
+      }
     }
+  }
+  for (int sp = 1; !fp8 && sp <= 8; sp *= 2) {
+    if (sp > 1 && kblocks < 4 * sp) break;
     const int64_t per_sm = (base * sp + sms - 1) / sms;
     if (sp > 1 && per_sm > cap) break;
     const int64_t cost = per_sm * ((kblocks + sp - 1) / sp);
@@ -282,7 +302,7 @@ sp24_status make_plan(int64_t m, int64_t n, int kblocks, int dtype, Plan* p) {
   p->impl = kSplitK;
   p->bn = bn;
   p->split = split;
-  p->small_ring = base * split > sms;
+  p->small_ring = base * split > sms && bn != 96;
   p->ctas = base * split;
   p->cluster = split;
   p->tile_tokens = bn;
@@ -382,6 +402,9 @@ sp24_status dispatch(const void* x, const void* vals, GemmArgs a, cudaStream_t s
   SP24_GEMM_CASE(32, (kDtype == SP24_FP8 ? 7 : 8))   // the scale buffers take one stage
   SP24_GEMM_CASE(64, 6)
   SP24_GEMM_CASE(128, 4)
+  if constexpr (kDtype == SP24_FP8) {
+    if (bn == 96) return launch_split<kDtype, 96, 5>(split, ma, mb, a, s);
+  }
 #undef SP24_GEMM_CASE
   return SP24_ERR_UNSUPPORTED;
 }

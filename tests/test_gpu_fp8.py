@@ -755,3 +755,14 @@ def test_gemm_scales_far_apart(m, ex, ew):
     assert B.sp24_device_status() == B.SP24_OK
     # the codes are whole multiples of 2^6 (three times 2^7 and below: 3 * 2^7 <= 448)
     np.testing.assert_array_equal(f64(y), f64(one) * 2.0 ** (ex - 127 + ew - 127))
+
+
+@pytest.mark.parametrize("m", [65, 95, 96, 97, 191, 192, 193, 288])
+@pytest.mark.parametrize("n,k", [(136, 800), (1032, 2048)])
+def test_gemm_at_the_borders_of_96_token_tiles(m, n, k):
+    xq, e_x, vals, meta, e_w, y, a = product_case(m, n, k, m)
+    assert B.sp24_gemm_plan(m, n, k, B.SP24_FP8)["kernel"] == "splitk"
+    for kind in (B.SP24_OUT_BF16, B.SP24_OUT_F32):
+        out = P.gemm_fp8(xq, e_x, vals, meta, e_w, n, kind)
+        assert B.sp24_device_status() == B.SP24_OK
+        assert_product(out, y, a, k, kind == B.SP24_OUT_BF16)
