@@ -354,7 +354,8 @@ __device__ __forceinline__ void norm_row_end(const NormArgs& a, int64_t row, int
 }
 
 // Rows straight from global memory: short rows (one warp each) and few rows.
-template <typename T, int OUT, int NV, bool kWarpRow, int MAXT, int MINB>
+// kRes: a residual may be given (its vectors take registers).
+template <typename T, int OUT, int NV, bool kWarpRow, int MAXT, int MINB, bool kRes = true>
 __global__ void __launch_bounds__(MAXT, MINB) norm_kernel(const NormArgs a) {
   pdl_launch_dependents();
   pdl_wait_prior();
@@ -364,7 +365,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_kernel(const NormArgs a) {
   const int per_cta = kWarpRow ? static_cast<int>(blockDim.x >> 5) : 1;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * per_cta + (kWarpRow ? threadIdx.x >> 5 : 0);
   const int64_t step = static_cast<int64_t>(gridDim.x) * per_cta;
-  const bool res = a.r != nullptr;
+  const bool res = kRes && a.r != nullptr;
   const int c_end = static_cast<int>(a.k / 8);
   const float sx = OUT == SP24_INT8 ? *a.s_x : 1.0f;
   const float rsx = __frcp_rn(sx);
@@ -385,8 +386,8 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_kernel(const NormArgs a) {
     }
   };
   // the next row is loaded before this one is reduced, where the registers
-  // allow (two float32 rows of two vectors would spill)
-  constexpr bool kAhead = sizeof(T) * NV <= 4 || kWarpRow;
+  // allow (two float32 rows of two vectors and their residuals would spill)
+  constexpr bool kAhead = sizeof(T) * NV <= 4 || kWarpRow || !kRes;
   if (kAhead && first < a.m) load(first);
   uint32_t buf = 0;
   for (int64_t row = first; row < a.m; row += step, buf ^= 1u) {
@@ -852,9 +853,9 @@ static sp24_status resident_blocks(const void* kern, Occupancy& o, int threads, 
   return SP24_OK;
 }
 
-template <typename T, int OUT, int NV, bool kWarpRow, int MAXT, int MINB>
+template <typename T, int OUT, int NV, bool kWarpRow, int MAXT, int MINB, bool kRes = true>
 static sp24_status launch_norm_t(const NormArgs& a, int threads, cudaStream_t s) {
-  auto kern = norm_kernel<T, OUT, NV, kWarpRow, MAXT, MINB>;
+  auto kern = norm_kernel<T, OUT, NV, kWarpRow, MAXT, MINB, kRes>;
   static Occupancy occ;
   int per_sm = 0;
   SP24_TRY(resident_blocks(reinterpret_cast<const void*>(kern), occ, threads, 0, &per_sm));
@@ -879,8 +880,14 @@ static sp24_status launch_norm(const NormArgs& a, cudaStream_t s) {
   // bytes in flight (8192 x 4096: 39.7 us, one vector 45.1, four 41.8).
   if (c <= 1024 && (c <= 128 || sizeof(T) == 4 || a.m <= 2 * sm_count()))
     return launch_norm_t<T, OUT, 1, false, 1024, 1>(a, round32(c), s);
-  if (c > 1024 && c <= 1536 && sizeof(T) == 4)
-    return launch_norm_t<T, OUT, 2, false, 768, 2>(a, round32((c + 1) / 2), s);
+  // Long float32 rows without a residual, more than one an SM: three vectors a
+  // thread, whose registers hold the next row as well (777 x 11008: 12.8 us, two
+  // vectors without the next row 14.0; 2000 x 11008: 28.6 and 32.2).  With a
+  // residual, or a row an SM, two vectors (100 x 11008: 3.8 us, three 5.1).
+  if constexpr (sizeof(T) == 4) {
+    if (c > 1024 && c <= 1536 && a.r == nullptr && a.m > sm_count())
+      return launch_norm_t<T, OUT, 3, false, 512, 2, false>(a, round32((c + 2) / 3), s);
+  }
   return launch_norm_t<T, OUT, 2, false, 1024, 1>(a, round32((c + 1) / 2), s);
 }
 

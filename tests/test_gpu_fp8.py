@@ -766,3 +766,30 @@ def test_gemm_at_the_borders_of_96_token_tiles(m, n, k):
         out = P.gemm_fp8(xq, e_x, vals, meta, e_w, n, kind)
         assert B.sp24_device_status() == B.SP24_OK
         assert_product(out, y, a, k, kind == B.SP24_OUT_BF16)
+
+
+@pytest.mark.parametrize("m", [148, 149, 500])
+@pytest.mark.parametrize("k", [8208, 11008, 12288, 12304])
+def test_norm_of_long_float_rows(m, k):
+    """Float32 rows past the one-vector kernels, with the next row in registers
+    (more rows than SMs, no residual) and without; every output type."""
+    x, gamma = rand((m, k), F32, m + k), 1.0 + 0.1 * rand((1, k), F32, k)[0]
+    r = rand((m, k), F32, 3 * m + k)
+    sx = torch.tensor([0.05], device="cuda")
+    for res in (None, r):
+        h = x if res is None else x + res
+        y, s = O.rmsnorm(f64(h), f64(gamma), EPS)
+        rc = None if res is None else res.cuda()
+        q = P.rmsnorm_quant(x.cuda(), gamma.cuda(), rc, EPS, want_rstd=True)
+        assert torch.equal(q.h.cpu(), h)
+        assert (np.abs(f64(q.rstd) - s) <= NORM_REL * s).all()
+        e = np.repeat(exps(q.e_y)[:, :(k + 127) // 128], 128, axis=1)[:, :k]
+        # half a code step, and the arithmetic's error
+        step = np.maximum(2.0 ** -4 * np.abs(y) * (1 + NORM_REL), 2.0 ** (e - 10.0))
+        assert (np.abs(f64(q.y) * 2.0 ** e - y) <= step + NORM_REL * np.abs(y)).all()
+        b = P.rmsnorm_quant(x.cuda(), gamma.cuda(), rc, EPS, B.SP24_BF16)
+        assert (np.abs(f64(b.y) - y) <= (HALF_BF16 + 2 * NORM_REL) * np.abs(y)).all()
+        i = P.rmsnorm_quant(x.cuda(), gamma.cuda(), rc, EPS, B.SP24_INT8, s_x=sx)
+        z = np.clip(y / float(sx.cpu()[0]), -127, 127)
+        assert (np.abs(i.y.cpu().numpy() - z) <= 0.5 + 2 * NORM_REL * np.abs(z)).all()
+    assert B.sp24_device_status() == B.SP24_OK
