@@ -201,14 +201,18 @@ sp24_status make_plan(int64_t m, int64_t n, int kblocks, int dtype, Plan* p) {
   // (an SP24_GEMM_IMPL override applies from half a wave of tiles, as the
   // kernel-family tests expect)
   const int64_t tiles128 = row_tiles * ((m + 127) / 128);
-  if (forced != kSplitK && m >= 128 && tiles128 >= (forced >= 0 ? sms / 2 : sms) &&
-      !(fp8 && forced < 0 && (m < 256 || (n < 256 && m <= 65535 * 128)))) {
+  // e4m3 has no single-SM kernel: what a pair tile cannot fill goes to split-K,
+  // unless its tiles are more than a launch's y and z number (16 bits each)
+  const bool fp8_split =
+      fp8 && forced < 0 && (m < 256 || n < 256) && row_tiles <= 65535 && m <= 65535 * 128;
+  const bool enough = m >= 128 || (fp8 && row_tiles > 65535);
+  if (forced != kSplitK && enough && tiles128 >= (forced >= 0 ? sms / 2 : sms) && !fp8_split) {
     int pairs = 0;
     SP24_TRY(pair_capacity(&pairs));
     int impl = forced;
     if (impl < 0) {
       impl = kSingle;   // pair tiles need both dimensions to fill them
-      if (m >= 256 && n >= 256) {
+      if (fp8 || (m >= 256 && n >= 256)) {
         double best = fp8 ? 1e30 : est_time(kSingle, m, n, kblocks, sms, pairs, false);
         for (int c : {kPair256, kPair240, kPair224}) {
           const double t = est_time(c, m, n, kblocks, sms, pairs, fp8);
