@@ -479,7 +479,8 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_fp8_kernel(const Quant
   for (int u = 0; u < kQuantUnroll; ++u) {
     const uint32_t b = b0 + u * kHalves;
     const uint32_t row = a.by_kb(b);
-    const bool ok = b < a.blocks && (b - row * a.kb) * 128 + 8 * t < a.k;
+    // columns end inside a row's last block only (a column may pass 32 bits)
+    const bool ok = b < a.blocks && (b - row * a.kb + 1 < a.kb || 8 * t + a.pad_cols < 128);
     at[u] = ok ? static_cast<int64_t>(b) * 128 + 8 * t - static_cast<int64_t>(row) * a.pad_cols : -1;
     x[u].zero();
     if (ok) x[u].load(static_cast<const T*>(a.x) + at[u]);

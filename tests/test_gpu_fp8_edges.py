@@ -62,3 +62,24 @@ def test_gemm_of_more_row_tiles_than_a_grid_numbers(m):
     y, a = O.fp8_gemm(f64(xq), exps(e_x)[:, :1], wq, we)
     assert_product(out[:, -t:], y, a, k, True)
     assert not out[:, :-t].any()
+
+
+# ----------------------------------------------------- columns past 32 bits
+def test_quantize_of_rows_longer_than_32_bits():
+    """The last block ends inside its 128 columns: what lies behind the row is
+    neither read into its scale nor written."""
+    k = 2 ** 32 + 16
+    x = torch.zeros(k + 256, dtype=BF, device="cuda")
+    x[k:] = 300.0                               # behind the row: would raise the scale
+    tail = rand((1, 144), BF, 1)
+    x[k - 144:k] = tail[0].cuda()
+    codes = torch.full((k + 256,), 0x55, dtype=torch.uint8, device="cuda")
+    q, e = P.quantize_fp8(x[:k].view(1, k), out=codes[:k].view(torch.float8_e4m3fn).view(1, k))
+    assert B.sp24_device_status() == B.SP24_OK
+    want_q, want_e = O.fp8_rows(f64(tail))       # k - 144 = 2^32 - 128: whole blocks before
+    np.testing.assert_array_equal(f64(q[:, -144:]), want_q)
+    ex = exps(e)[0]
+    blocks = (k + 127) // 128
+    np.testing.assert_array_equal(ex[blocks - 2:blocks], want_e[0])
+    assert (ex[:blocks - 2] == 0).all() and (ex[blocks:] == 0).all()
+    assert not codes[:k - 144].any() and (codes[k:] == 0x55).all()
