@@ -244,38 +244,48 @@ __device__ __forceinline__ Vec8<T> norm_sum(const Vec8<T>& x, const Vec8<T>& r, 
 // of two bf16 values is exact in fp32, that of two floats is taken with its
 // remainder.
 //
-// kOdd: rounded to odd (truncated, last bit set), for a y that is rounded again
-// to a code: every border between codes is an even fp32 number, so y stays on
-// the side of the border that the exact product is on, and only the error of s
-// can still move a code (8192 x 4096: 1 to 23 of 33.5 million codes differ from
-// those of 64 bits, 20 to 27 with y rounded to nearest, 19 to 38 in plain fp32).
-// `last` is the bit to set in both halves: an inexact product is needed, which
-// lo != 0 makes it, so it is 0 for a row with lo == 0.  A zero becomes the
-// smallest subnormal.
-template <bool kOdd>
+// kOdd: rounded to odd (truncated, last bit set if that left something), for a y
+// that is rounded again to a code: every border between codes is an even fp32
+// number, so y stays on the side of the border that the exact product is on, and
+// only the error of s can still move a code (8192 x 4096: 1 to 23 of 33.5 million
+// codes differ from those of 64 bits, 20 to 27 with y rounded to nearest, 19 to
+// 38 in plain fp32).
+// `last` is the bit to set in both halves.  s is irrational, so no product with
+// it is exact and the bit is set in all (a zero becomes the smallest subnormal),
+// unless s is a power of two: then only float32 products that fp32 does not
+// hold are inexact, those with a remainder (kAsk).  Rows of this kind are rare:
+// they are done again after the others, as the question in every row, or a loop
+// of its own there, costs registers (777 x 11008: 15.3 us a call; 14.0 this way
+// and 13.9 without).
+enum Rounding { kNearest, kOdd, kAsk };
+
+__device__ __forceinline__ bool norm_pow2(float2 s) {
+  return s.y == 0.0f && (__float_as_uint(s.x) & 0x007FFFFFu) == 0u;
+}
+
+template <Rounding R>
 __device__ __forceinline__ Pair norm_round(Pair p, Pair s, Pair rest, uint64_t last) {
-  if constexpr (!kOdd) return fma2(p, s, rest);
+  if constexpr (R == kNearest) return fma2(p, s, rest);
   Pair y = fma2_rz(p, s, rest);
   y.v |= last;
   return y;
 }
-template <bool kOdd>
+template <Rounding R>
 __device__ __forceinline__ void norm_scale(const Vec8<__nv_bfloat16>& h, const Vec8<__nv_bfloat16>& g,
                                            float2 s, Pair (&y)[4]) {
-  const uint64_t last = s.y != 0.0f ? 0x0000000100000001ull : 0ull;
+  const uint64_t last = norm_pow2(s) ? 0ull : 0x0000000100000001ull;
   Pair fg[4];
   h.get(y);
   g.get(fg);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const Pair p = mul2(y[j], fg[j]);
-    y[j] = norm_round<kOdd>(p, pair(s.x), mul2(p, pair(s.y)), last);
+    y[j] = norm_round<R>(p, pair(s.x), mul2(p, pair(s.y)), last);
   }
 }
-template <bool kOdd>
+template <Rounding R>
 __device__ __forceinline__ void norm_scale(const Vec8<float>& h, const Vec8<float>& g, float2 s,
                                            Pair (&y)[4]) {
-  const uint64_t last = s.y != 0.0f ? 0x0000000100000001ull : 0ull;
   Pair fg[4];
   h.get(y);
   g.get(fg);
@@ -283,18 +293,24 @@ __device__ __forceinline__ void norm_scale(const Vec8<float>& h, const Vec8<floa
   for (int j = 0; j < 4; ++j) {
     const Pair p = mul2(y[j], fg[j]);
     const Pair e = fma2(y[j], fg[j], mul2(p, pair(-1.0f)));
-    y[j] = norm_round<kOdd>(p, pair(s.x), fma2(p, pair(s.y), mul2(e, pair(s.x))), last);
+    uint64_t last = 0x0000000100000001ull;
+    if constexpr (R == kAsk) {
+      float e0, e1;
+      split(e, e0, e1);
+      last = (e0 != 0.0f ? 1ull : 0ull) | (e1 != 0.0f ? 1ull << 32 : 0ull);
+    }
+    y[j] = norm_round<R>(p, pair(s.x), fma2(p, pair(s.y), mul2(e, pair(s.x))), last);
   }
 }
 
 // y of one vector (columns 8c ..) of row `row` and its output.  All lanes of a
 // warp call it, `ok` where the columns exist: 16 neighbouring lanes hold a
 // 128-column block.
-template <typename T, int OUT>
+template <typename T, int OUT, Rounding R = OUT == SP24_FP8 ? kOdd : kNearest>
 __device__ __forceinline__ void norm_out(const NormArgs& a, const Vec8<T>& h, const Vec8<T>& g,
                                          float2 rs, int64_t row, int c, bool ok, float sx, float rsx) {
   Pair y[4];
-  norm_scale<OUT == SP24_FP8>(h, g, rs, y);
+  norm_scale<R>(h, g, rs, y);
   float f[8];
 #pragma unroll
   for (int j = 0; j < 4; ++j) split(y[j], f[2 * j], f[2 * j + 1]);
@@ -389,6 +405,9 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_kernel(const NormArgs a) {
   // allow (two float32 rows of two vectors and their residuals would spill)
   constexpr bool kAhead = sizeof(T) * NV <= 4 || kWarpRow || !kRes;
   if (kAhead && first < a.m) load(first);
+  // e4m3 codes of float32 rows whose s is a power of two: see norm_scale
+  constexpr bool kAskAgain = OUT == SP24_FP8 && sizeof(T) == 4;
+  bool again = false;
   uint32_t buf = 0;
   for (int64_t row = first; row < a.m; row += step, buf ^= 1u) {
     if (!kAhead) load(row);
@@ -406,6 +425,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_kernel(const NormArgs a) {
     const float2 rs = norm_rstd(
         row_sum<kWarpRow, double>(sum + odd, part[buf], threadIdx.x >> 5, blockDim.x >> 5, 0), a);
     norm_row_end<OUT>(a, row, t, rs);
+    if (kAskAgain) again |= rs.y == 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = t + i * nt;
@@ -413,6 +433,41 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_kernel(const NormArgs a) {
       g.zero();
       if (c < c_end) g.load_cached(static_cast<const T*>(a.gamma) + 8 * c);
       norm_out<T, OUT>(a, h[i], g, rs, row, c, c < c_end, sx, rsx);
+    }
+  }
+  if constexpr (kAskAgain) {   // rows with such an s are written again (the same
+    if (!again) return;        // answer in all of a row's threads)
+    for (int64_t row = first; row < a.m; row += step, buf ^= 1u) {
+      // h is read again, as stored (x may be overwritten by it)
+      const T* hp = static_cast<const T*>(a.h != nullptr ? a.h : a.x) + row * a.k;
+      const bool add = res && a.h == nullptr;
+      Vec8<T> h[NV];
+      Pair sum2 = pair(0.0f);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = t + i * nt;
+        Vec8<T> v, w;
+        v.zero();
+        w.zero();
+        if (c < c_end) {
+          v.load(hp + 8 * c);
+          if (add) w.load(static_cast<const T*>(a.r) + row * a.k + 8 * c);
+        }
+        h[i] = norm_sum<T>(v, w, add, sum2);
+      }
+      float sum, odd;
+      split(sum2, sum, odd);
+      const float2 rs = norm_rstd(
+          row_sum<kWarpRow, double>(sum + odd, part[buf], threadIdx.x >> 5, blockDim.x >> 5, 0), a);
+      if (!norm_pow2(rs)) continue;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = t + i * nt;
+        Vec8<T> g;
+        g.zero();
+        if (c < c_end) g.load_cached(static_cast<const T*>(a.gamma) + 8 * c);
+        norm_out<T, OUT, kAsk>(a, h[i], g, rs, row, c, c < c_end, sx, rsx);
+      }
     }
   }
 }

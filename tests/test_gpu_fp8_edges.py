@@ -83,3 +83,66 @@ def test_quantize_of_rows_longer_than_32_bits():
     np.testing.assert_array_equal(ex[blocks - 2:blocks], want_e[0])
     assert (ex[:blocks - 2] == 0).all() and (ex[blocks:] == 0).all()
     assert not codes[:k - 144].any() and (codes[k:] == 0x55).all()
+
+
+# -------------------------------------------- rows whose 1 / rms is exact
+def exact_root_rows(m, k, rng):
+    """Whole numbers up to 255 of both signs whose squares sum to k * 64^2: every
+    partial sum is exact in fp32 and 1 / rms = 2^-6."""
+    h = np.zeros((m, k), dtype=np.int64)
+    for i in range(m):
+        while True:
+            a = rng.integers(1, 110, k)
+            rest = k * 4096 - int((a[:-4] ** 2).sum())
+            p = np.arange(256) ** 2
+            two = (p[:, None] + p[None, :]).ravel()
+            first = np.full(2 * 255 ** 2 + 1, -1)
+            first[two] = np.arange(two.size)
+            for t in range(max(rest - 2 * 255 ** 2, 0), min(rest, 2 * 255 ** 2) + 1):
+                if first[t] >= 0 and first[rest - t] >= 0:
+                    a[-4:] = [first[t] // 256, first[t] % 256, first[rest - t] // 256,
+                              first[rest - t] % 256]
+                    break
+            else:
+                continue
+            break
+        h[i] = a * rng.choice([-1, 1], k)
+        assert (h[i] ** 2).sum() == k * 4096
+    return h
+
+
+@pytest.mark.parametrize("m,k", [(3, 256), (2, 512), (3, 2048), (2, 4096), (2, 16384)])
+def test_norm_rounds_products_of_an_exact_root_once(m, k):
+    """Float32 products a little above a tie of the code or above 448 * 2^e, with
+    an s that has no remainder: the part that fp32 cannot hold still decides."""
+    rng = np.random.default_rng(k)
+    h = exact_root_rows(m, k, rng)
+    h[1:] = h[0]                               # (one gamma aims at every row)
+    h[1:, :k // 2] *= -1
+    top = np.where(np.arange(k) % 128 == 5, 448.0 * 2.0 ** (np.arange(k) // 128 % 3), 0.0)
+    tie = np.array([17.0, 19.0, 21.0, 23.0, 25.0, 27.0, 29.0, 31.0])[rng.integers(0, 8, k)]
+    want = np.where(top > 0, top, tie * 2.0 ** rng.integers(-3, 3, k))
+    mag = np.maximum(np.abs(h[0]), 1)
+    gamma = (want * 64 / mag).astype(np.float32)
+    low = gamma.astype(np.float64) * mag < want * 64
+    gamma = np.where(low, np.nextafter(gamma, np.float32(np.inf)), gamma).astype(np.float32)
+    y = h * gamma.astype(np.float64) / 64
+    inexact = y.astype(np.float32).astype(np.float64) != y
+    assert inexact.mean() > 0.3
+    x = torch.from_numpy(h.astype(np.float32)).cuda()
+    o = P.rmsnorm_quant(x, torch.from_numpy(gamma).cuda(), eps=0.0, want_rstd=True)
+    assert o.rstd.cpu().tolist() == [2.0 ** -6] * m
+    want_q, want_e = O.fp8_rows(y)
+    np.testing.assert_array_equal(exps(o.e_y)[:, :k // 128], want_e)
+    np.testing.assert_array_equal(f64(o.y), want_q)
+    # the same sum of two streams: stored over either, apart, and not at all
+    g = torch.from_numpy(gamma).cuda()
+    r = torch.from_numpy(rng.integers(-64, 65, (m, k)).astype(np.float32)).cuda()
+    for target in ("x", "r", "new", "none"):
+        a, b = x - r, r.clone()
+        q, e = torch.empty_like(o.y), torch.empty_like(o.e_y)
+        h = {"x": a, "r": b, "new": torch.empty_like(a), "none": None}[target]
+        B.sp24_rmsnorm_quant(a, b, g, 0.0, B.SP24_FP8, None, h, q, e, None)
+        assert torch.equal(q.view(torch.uint8), o.y.view(torch.uint8))
+        assert torch.equal(e.view(torch.uint8), o.e_y.view(torch.uint8))
+        assert h is None or torch.equal(h, x)
