@@ -433,7 +433,12 @@ sp24_status sp24_gemm_fp8(const void* X, const uint8_t* e_x, int64_t M, int64_t 
  * for SP24_FP8, s_x (one float32, device) for SP24_INT8; pointers 16-byte
  * aligned (rstd and s_x: 4).  A row of zeros gives zeros when eps > 0.  A y that
  * overflows fp32 (or, for SP24_FP8, comes within 2^-23 of its largest number)
- * counts as an infinity. */
+ * counts as an infinity.
+ * Range: h * gamma is formed before s is applied, and squares before their sum,
+ * both in fp32.  A product past 3.4e38 makes its e4m3 block NaN (an int8 or bf16
+ * output of it has no meaning) even where y would be finite; a row whose squares
+ * sum to more counts as one with an infinite root (s = 0); squares below 2^-149
+ * count as 0. */
 sp24_status sp24_rmsnorm_quant(const void* X, const void* R, const void* gamma, int64_t M,
                                int64_t K, int x_dtype, float eps, int out_dtype, const float* s_x,
                                void* H, void* Y, uint8_t* e_y, float* rstd, void* stream);
@@ -452,7 +457,8 @@ size_t sp24_rmsnorm_backward_workspace_bytes(int64_t M, int64_t K);
  *   dgamma: float32 [K] (zeros for M = 0).
  *   workspace: sp24_rmsnorm_backward_workspace_bytes(M, K) bytes, in use until
  *   the call's kernels have finished: calls that may overlap need one each.
- * Rules: as sp24_rmsnorm_quant. */
+ * Rules: as sp24_rmsnorm_quant; the products dY * H and dY * gamma have to stay
+ * within fp32's range. */
 sp24_status sp24_rmsnorm_backward(const void* dY, const void* dH, const void* H, const void* gamma,
                                   const float* rstd, int64_t M, int64_t K, int x_dtype, void* dX,
                                   float* dgamma, void* workspace, size_t workspace_bytes,

@@ -146,3 +146,24 @@ def test_norm_rounds_products_of_an_exact_root_once(m, k):
         assert torch.equal(q.view(torch.uint8), o.y.view(torch.uint8))
         assert torch.equal(e.view(torch.uint8), o.e_y.view(torch.uint8))
         assert h is None or torch.equal(h, x)
+
+
+# ------------------------------------------------ the range that sp24.h states
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("k", [512, 2048])
+def test_norm_range_of_products_and_squares(k, dt):
+    """A product h * gamma past float32 makes its block NaN and no other; squares
+    past it, a row of zeros."""
+    x = torch.ones((3, k), dtype=dt)
+    x[1] = 2.0 ** 30
+    x[2] = 2.0 ** 70                           # squares past 2^128
+    gamma = torch.ones(k, dtype=dt)
+    gamma[3] = 2.0 ** 99                       # y of 2^99; times 2^30 past 2^128
+    o = P.rmsnorm_quant(x.cuda(), gamma.cuda(), eps=0.0, want_rstd=True)
+    assert o.rstd.cpu().tolist() == [1.0, 2.0 ** -30, 0.0]
+    by, q = o.e_y.view(torch.uint8).cpu(), o.y.view(torch.uint8).cpu()
+    assert exps(o.e_y)[0, 0] == 99 - 8 and f64(o.y)[0, 3] == 256
+    # (2^30 and 2^70 times 2^99 both pass 2^128: rows 1 and 2)
+    assert (by[1:, 0] == 255).all() and (q[1:, :128] == 0x7F).all()
+    assert (exps(o.e_y)[:2, 1:k // 128] == -8).all() and (f64(o.y)[:2, 128:] == 256).all()
+    assert (f64(o.y)[2, 128:] == 0).all()
