@@ -344,4 +344,12 @@ PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, method
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&module_def); }
+// built_for: the Python and torch this was compiled against (build.py).
+PyMODINIT_FUNC PyInit__binding() {
+  PyObject* m = PyModule_Create(&module_def);
+  if (m != nullptr && PyModule_AddStringConstant(m, "built_for", SP24_BINDING_TAG) < 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

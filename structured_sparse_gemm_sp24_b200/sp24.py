@@ -161,16 +161,18 @@ _NATIVE_FUNCTIONS = ("sp24_quantize_fp8", "sp24_prune_compress_fp8", "sp24_compr
 
 def native():
     """The native half of the binding, bound to the loaded library.  Raises if
-    _binding.so has not been built."""
+    _binding.so has not been built for this Python and torch."""
     global _NATIVE
     if _NATIVE is None:
         h = lib()
+        how = "build it with `python -m structured_sparse_gemm_sp24_b200.build`"
         try:
             from . import _binding
         except ImportError as e:
-            raise RuntimeError(
-                "_binding.so is missing or does not load: build it with "
-                "`python -m structured_sparse_gemm_sp24_b200.build`") from e
+            raise RuntimeError(f"_binding.so is missing or does not load: {how}") from e
+        from .build import binding_tag
+        if _binding.built_for != binding_tag():
+            raise RuntimeError(f"_binding.so is a {_binding.built_for}, this is {binding_tag()}: {how}")
         _binding.bind(*(ctypes.cast(getattr(h, f), _c_p).value for f in _NATIVE_FUNCTIONS))
         _NATIVE = _binding
     return _NATIVE
