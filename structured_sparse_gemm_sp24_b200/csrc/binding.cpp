@@ -15,6 +15,8 @@
 #include <ATen/ATen.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
+#include <c10/util/Exception.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <exception>
@@ -114,6 +116,21 @@ void* stream_of(PyObject* o, int dev) {
   return p;
 }
 
+// The Python error of the C++ exception being handled: ValueError for a refused
+// tensor, torch's own for its errors (torch.OutOfMemoryError for an allocation
+// that fails, as torch.empty raises it), RuntimeError otherwise.
+void to_python() {
+  try {
+    throw;
+  } catch (const std::invalid_argument& e) {
+    PyErr_SetString(PyExc_ValueError, e.what());
+  } catch (const c10::Error&) {
+    torch::translate_exception_to_python(std::current_exception());
+  } catch (const std::exception& e) {
+    if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
+  }
+}
+
 // Runs `body`, which returns a status, with the argument count checked and C++
 // exceptions turned into Python ones.
 template <class Body>
@@ -122,10 +139,8 @@ PyObject* guarded(Py_ssize_t have, Py_ssize_t want, const void* bound, Body&& bo
     if (have != want) throw std::runtime_error("sp24: wrong number of arguments");
     if (bound == nullptr) throw std::runtime_error("sp24: the library is not loaded");
     return PyLong_FromLong(body());
-  } catch (const std::invalid_argument& e) {
-    PyErr_SetString(PyExc_ValueError, e.what());
-  } catch (const std::exception& e) {
-    if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (...) {
+    to_python();
   }
   return nullptr;
 }
@@ -265,10 +280,8 @@ PyObject* guarded_new(Py_ssize_t have, Py_ssize_t least, Py_ssize_t most, Body&&
   try {
     if (have < least || have > most) throw std::runtime_error("sp24: wrong number of arguments");
     return body();
-  } catch (const std::invalid_argument& e) {
-    PyErr_SetString(PyExc_ValueError, e.what());
-  } catch (const std::exception& e) {
-    if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (...) {
+    to_python();
   }
   return nullptr;
 }

@@ -167,3 +167,14 @@ def test_norm_range_of_products_and_squares(k, dt):
     assert (by[1:, 0] == 255).all() and (q[1:, :128] == 0x7F).all()
     assert (exps(o.e_y)[:2, 1:k // 128] == -8).all() and (f64(o.y)[:2, 128:] == 256).all()
     assert (f64(o.y)[2, 128:] == 0).all()
+
+
+# ------------------------------------------------------------------- errors
+def test_an_allocation_that_fails_raises_as_torch_does():
+    vals, meta, e_w = P.prune_compress_fp8(torch.zeros((64, 256), dtype=BF, device="cuda"))
+    xq, e_x = P.quantize_fp8(torch.zeros((1, 256), dtype=BF, device="cuda"))
+    with pytest.raises(torch.OutOfMemoryError, match="out of memory") as e:
+        P.gemm_fp8(xq, e_x, vals, meta, e_w, 1 << 48)         # an output of 2^49 bytes
+    assert "frame #" not in str(e.value)
+    assert B.sp24_device_status() == B.SP24_OK
+    assert P.gemm_fp8(xq, e_x, vals, meta, e_w, 64).shape == (1, 64)
