@@ -79,6 +79,8 @@ def save_compressed(path: str, vals: torch.Tensor, meta: torch.Tensor, n: int, k
     if (s_w is None) != (sc == 0) or (s_w is not None and s_w.numel() != sc):
         raise ValueError("int8 weights need their N float32 scales, e4m3 weights their block "
                          "scales, bf16 weights none")
+    if dtype == _b.SP24_FP8 and s_w.element_size() != 1:
+        raise ValueError("e4m3 block scales are bytes (float8_e8m0fnu or uint8)")
     hdr = _HEADER.pack(MAGIC, FORMAT_VERSION, LAYOUT_VERSION, dtype, 0, n, k, vb, mb, sc)
     tmp = path + ".tmp"
     with open(tmp, "wb") as f:
@@ -87,8 +89,6 @@ def save_compressed(path: str, vals: torch.Tensor, meta: torch.Tensor, n: int, k
         f.write(meta.detach().contiguous().cpu().view(torch.uint8).numpy().tobytes())
         if s_w is not None:
             if dtype == _b.SP24_FP8:
-                if s_w.element_size() != 1:
-                    raise ValueError("e4m3 block scales are bytes (float8_e8m0fnu or uint8)")
                 s_w = s_w.detach().contiguous().cpu().view(torch.uint8)
             else:
                 s_w = s_w.detach().to(torch.float32).contiguous().cpu()

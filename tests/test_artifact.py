@@ -95,3 +95,13 @@ def test_save_checks_sizes(tmp_path):
         A.save_compressed(str(tmp_path / "b"), v8, m8, n, k, B.SP24_INT8, None)
     with pytest.raises(ValueError):   # bf16 takes none
         A.save_compressed(str(tmp_path / "c"), vals, meta, n, k, B.SP24_BF16, torch.ones(n))
+
+
+def test_refused_save_leaves_no_file(tmp_path):
+    """A call with e4m3 scales of the wrong type is refused before anything is written."""
+    n, k = 130, 544
+    vals = torch.zeros((n, k // 2), dtype=torch.uint8).view(torch.float8_e4m3fn)
+    meta = torch.zeros(B.sp24_meta_bytes(n, k), dtype=torch.uint8)
+    with pytest.raises(ValueError, match="bytes"):
+        A.save_compressed(str(tmp_path / "w.sp24"), vals, meta, n, k, B.SP24_FP8, torch.ones(2, 8))
+    assert list(tmp_path.iterdir()) == []
