@@ -343,7 +343,8 @@ sp24_status sp24_gemm(const void* X, int64_t M, int64_t K, const void* vals,
  *   split_k:       K slices per tile (1 unless "splitk").
  *   ctas, cluster: CTAs launched and CTAs per cluster.
  * SP24_FP8 reports the launch of sp24_gemm_fp8, which has the kernels splitk
- * (splits 1, 2, 4, 8), pair256, pair240 and pair224; other overrides are ignored.
+ * (splits 1, 2, 4, 8, of them the ones with at most a CTA an SM), pair256, pair240
+ * and pair224; other overrides are ignored, a larger split is lowered.
  * Errors: SP24_ERR_ARG for a NULL plan, M < 1, N < 1, K < 16 or an unknown
  * dtype; SP24_ERR_CUDA if the device cannot be queried. */
 typedef struct sp24_gemm_plan_t {

@@ -302,7 +302,11 @@ sp24_status make_plan(int64_t m, int64_t n, int kblocks, int dtype, Plan* p) {
     }
   }
   const int so = split_override();
-  if (so > 0 && so <= kblocks) split = fp8 ? (so >= 8 ? 8 : so >= 4 ? 4 : so >= 2 ? 2 : 1) : so;
+  if (so > 0 && so <= kblocks) {
+    split = fp8 ? (so >= 8 ? 8 : so >= 4 ? 4 : so >= 2 ? 2 : 1) : so;
+    // (e4m3 CTAs share an SM only where the tiles alone are more than the SMs)
+    while (fp8 && split > 1 && base * split > sms) split /= 2;
+  }
   p->impl = kSplitK;
   p->bn = bn;
   p->split = split;
@@ -335,6 +339,18 @@ sp24_status launch_split(int split, const CUtensorMap& ma, const CUtensorMap& mb
       case 7: return launch_gemm_cfg<kDtype, BN, ST, 7>(ma, mb, a, s);
       default: return launch_gemm_cfg<kDtype, BN, ST, 8>(ma, mb, a, s);
     }
+  }
+}
+
+// The small ring (e4m3 takes it without a split only).
+template <int kDtype, int BN>
+sp24_status launch_small(int split, const CUtensorMap& ma, const CUtensorMap& mb,
+                         const GemmArgs& a, cudaStream_t s) {
+  constexpr int kStages = small_ring_stages(BN);
+  if constexpr (kDtype == SP24_FP8) {
+    return split == 1 ? launch_gemm_cfg<kDtype, BN, kStages, 1>(ma, mb, a, s) : SP24_ERR_UNSUPPORTED;
+  } else {
+    return launch_split<kDtype, BN, kStages>(split, ma, mb, a, s);
   }
 }
 
@@ -398,8 +414,7 @@ sp24_status dispatch(const void* x, const void* vals, GemmArgs a, cudaStream_t s
 
 #define SP24_GEMM_CASE(BN_, ST_)                                                          \
   if (bn == BN_) {                                                                        \
-    constexpr int kSm = small_ring_stages(BN_);                                           \
-    if (p.small_ring) return launch_split<kDtype, BN_, kSm>(split, ma, mb, a, s);          \
+    if (p.small_ring) return launch_small<kDtype, BN_>(split, ma, mb, a, s);               \
     return launch_split<kDtype, BN_, ST_>(split, ma, mb, a, s);                             \
   }
   SP24_GEMM_CASE(16, 8)

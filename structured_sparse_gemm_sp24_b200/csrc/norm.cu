@@ -1018,10 +1018,11 @@ static sp24_status launch_back(const BackArgs& a, float* dgamma, cudaStream_t s)
   if (c <= 1024) return launch_back_t<T, 2>(a, round32((c + 1) / 2), dgamma, s);
   const int64_t row = a.k * static_cast<int64_t>(sizeof(T));
   const int64_t slots = (kBackRing - row) / ((a.dh ? 3 : 2) * row);
-  if (slots >= 2)
-    return launch_back_ring<T, 2>(a, round32((c + 1) / 2),
-                                  static_cast<int>(slots < kBackSlots ? slots : kBackSlots), dgamma, s);
-  return launch_back_t<T, 4>(a, round32((c + 3) / 4), dgamma, s);   // two float32 rows do not fit
+  if constexpr (sizeof(T) == 4)   // two float32 rows may not fit (bf16 rows always do)
+    if (slots < 2) return launch_back_t<T, 4>(a, round32((c + 3) / 4), dgamma, s);
+  static_assert(kBackRing >= 7 * SP24_NORM_MAX_K * 2, "two bf16 rows of dy, h and dh, and gamma");
+  return launch_back_ring<T, 2>(a, round32((c + 1) / 2),
+                                static_cast<int>(slots < kBackSlots ? slots : kBackSlots), dgamma, s);
 }
 
 }  // namespace sp24

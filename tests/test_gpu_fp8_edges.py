@@ -178,3 +178,22 @@ def test_an_allocation_that_fails_raises_as_torch_does():
     assert "frame #" not in str(e.value)
     assert B.sp24_device_status() == B.SP24_OK
     assert P.gemm_fp8(xq, e_x, vals, meta, e_w, 64).shape == (1, 64)
+
+
+def test_a_forced_split_keeps_one_cta_an_sm(monkeypatch):
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    for m in (1, 20, 40, 100):
+        for tiles in (3, 40, 80, sms + 2):
+            n = 128 * tiles
+            for split in range(1, 9):
+                monkeypatch.setenv("SP24_SPLITK", str(split))
+                p = B.sp24_gemm_plan(m, n, 4096, B.SP24_FP8)
+                assert p["kernel"] == "splitk" and p["split_k"] in (1, 2, 4, 8)
+                assert p["split_k"] <= split and (p["ctas"] <= sms or p["split_k"] == 1)
+    # a split that would share SMs is lowered, and the product is right
+    xq, e_x, vals, meta, e_w, y, a = product_case(20, 128 * 40, 1312, 3)
+    for split in (1, 2, 4, 8):
+        monkeypatch.setenv("SP24_SPLITK", str(split))
+        out = P.gemm_fp8(xq, e_x, vals, meta, e_w, 128 * 40)
+        assert B.sp24_device_status() == B.SP24_OK
+        assert_product(out, y, a, 1312, True)
