@@ -167,12 +167,63 @@ struct Plan {
 // Split-K rings: the full ring (one CTA per SM) and a small one with which
 // several split CTAs share an SM (so that a split spreads a few row tiles
 // over every SM without a second wave).  Shared memory per SM on sm_100 is
-// 228 KiB, of which each resident CTA also takes 1 KiB.  With either ring
-// the CTAs that fit an SM by shared memory need at most 512 tensor-memory
-// columns together (16 tokens: 3 x 32; 32: 4 x 64; 64: 3 x 128; 128:
-// 2 x 256), so no CTA's allocation ever waits on another's.
+// 228 KiB, of which each resident CTA also takes 1 KiB.  No CTA's allocation of
+// tensor memory may ever wait on another's: a CTA allocates before it waits for
+// the previous kernel, and the CTAs of a cluster wait for one another.  So the
+// CTAs that fit an SM by shared memory, of whatever types and token counts, need
+// at most 512 columns together (the worst mix is two 128-token CTAs of 256), and
+// any other kernel that uses tensor memory leaves no room beside it.
 constexpr int kSmemPerSm = 228 * 1024;
 constexpr int small_ring_stages(int bn) { return bn == 16 ? 3 : 2; }
+
+struct CtaNeeds {
+  int smem, columns;
+};
+template <class C>
+constexpr CtaNeeds needs_of() {
+  return {C::kSmemBytes + 1024, C::kTmemCols};
+}
+template <int kDtype, int BN>
+constexpr CtaNeeds kSmallRing = needs_of<GemmCfg<kDtype, BN, small_ring_stages(BN)>>();
+constexpr CtaNeeds kSmallRings[] = {
+    kSmallRing<SP24_BF16, 16>, kSmallRing<SP24_BF16, 32>, kSmallRing<SP24_BF16, 64>,
+    kSmallRing<SP24_BF16, 128>, kSmallRing<SP24_INT8, 16>, kSmallRing<SP24_INT8, 32>,
+    kSmallRing<SP24_INT8, 64>, kSmallRing<SP24_INT8, 128>, kSmallRing<SP24_FP8, 16>,
+    kSmallRing<SP24_FP8, 32>, kSmallRing<SP24_FP8, 64>, kSmallRing<SP24_FP8, 128>};
+
+// Most columns that small-ring CTAs number `from` and up can need in `smem` bytes.
+constexpr int most_columns(int smem, int from = 0) {
+  int best = 0;
+  for (int i = from; i < 12; ++i)
+    if (kSmallRings[i].smem <= smem) {
+      const int c = kSmallRings[i].columns + most_columns(smem - kSmallRings[i].smem, i);
+      best = c > best ? c : best;
+    }
+  return best;
+}
+static_assert(most_columns(kSmemPerSm) <= 512, "an allocation of tensor memory could wait");
+
+template <class C>
+constexpr bool fills_sm() {
+  return most_columns(kSmemPerSm - needs_of<C>().smem) == 0;
+}
+template <int kDtype>
+constexpr bool full_rings_fill_sm() {
+  return fills_sm<GemmCfg<kDtype, 16, 8>>() && fills_sm<GemmCfg<kDtype, 32, 7>>() &&
+         fills_sm<GemmCfg<kDtype, 64, 6>>() && fills_sm<GemmCfg<kDtype, 128, 4>>();
+}
+static_assert(full_rings_fill_sm<SP24_BF16>() && full_rings_fill_sm<SP24_INT8>() &&
+                  full_rings_fill_sm<SP24_FP8>() && fills_sm<GemmCfg<SP24_FP8, 96, 5>>(),
+              "a split-K CTA with the full ring shares its SM");
+// (the pair and single-SM variants with the least shared memory)
+static_assert(fills_sm<PairCfg<SP24_BF16, 192, 4, SP24_OUT_BF16, 2>>() &&
+                  fills_sm<PairCfg<SP24_INT8, 240, 3, SP24_OUT_INT32, 2>>() &&
+                  fills_sm<PairCfg<SP24_FP8, 256, 3, SP24_OUT_BF16, 1>>() &&
+                  fills_sm<PairCfg<SP24_FP8, 224, 3, SP24_OUT_F32, 2>>() &&
+                  fills_sm<PersistCfg<SP24_BF16, 112, 4, SP24_OUT_BF16>>() &&
+                  fills_sm<PersistCfg<SP24_INT8, 112, 3, SP24_OUT_INT32>>() &&
+                  fills_sm<PersistCfg<SP24_INT8, 112, 4, SP24_OUT_INT8>>(),
+              "a persistent CTA shares its SM");
 
 template <int kDtype>
 int small_ring_smem(int bn) {

@@ -5,8 +5,8 @@
 // blocks of one tile; their partial accumulators are summed in a fixed order
 // through distributed shared memory, so the result does not depend on timing.
 //
-// Warp roles (128 threads): warp 0 lane 0 issues TMA, warp 1 lane 0 issues
-// tcgen05 (copy + MMA), warp 2 owns the tensor-memory allocation, warp 3 lays
+// Warp roles (128 threads): an elected thread of warp 0 issues TMA, one of warp 1
+// issues tcgen05 (copy + MMA), warp 2 owns the tensor-memory allocation, warp 3 lays
 // out the block scales of an e4m3 product (gemm_fp8.cuh); all four
 // warps run the epilogue (tcgen05.ld of their 32 lanes -> scale / cast ->
 // shared-memory transpose -> coalesced 16-byte stores of Y rows).
