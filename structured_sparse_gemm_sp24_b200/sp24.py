@@ -202,6 +202,13 @@ def _ptr(t: Optional[torch.Tensor]):
     return t.data_ptr()
 
 
+def _f32(t: torch.Tensor, name: str) -> None:
+    """Refuses a tensor that the library would read as float32 and that is not (a
+    shorter type would be read past its end)."""
+    if t.dtype != torch.float32:
+        raise ValueError(f"sp24: {name} must be float32, not {t.dtype}")
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:   # (current_stream() builds a Python object: 3 us a call)
         return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
@@ -276,11 +283,14 @@ def sp24_wscale(W: torch.Tensor, mask: torch.Tensor, coverage: float, s_w: torch
 
 def sp24_act_scale(X: torch.Tensor, coverage: float, s_x: torch.Tensor,
                    workspace: torch.Tensor, stream=None) -> None:
+    _f32(X, "X")
     _check(lib().sp24_act_scale(_ptr(X), X.numel(), float(coverage), _ptr(s_x),
                                 _ptr(workspace), _stream(stream)), "sp24_act_scale")
 
 
 def sp24_quantize(X: torch.Tensor, s_x: torch.Tensor, Xq: torch.Tensor, stream=None) -> None:
+    _f32(X, "X")
+    _f32(s_x, "s_x")
     _check(lib().sp24_quantize(_ptr(X), X.numel(), _ptr(s_x), _ptr(Xq), _stream(stream)),
            "sp24_quantize")
 

@@ -247,3 +247,17 @@ def test_conv3x3_host_validation(lib):
     assert call(meta=None) == B.SP24_ERR_ARG
     assert call(B=-1) == B.SP24_ERR_ARG
     assert call(B=0) == B.SP24_OK and call(Cout=0) == B.SP24_OK
+
+
+def test_float32_inputs_are_checked(lib):
+    """The int8 calibration reads float32: another type is refused before any CUDA
+    call, not read past its end."""
+    import torch
+    f, h = torch.zeros(64), torch.zeros(64, dtype=torch.bfloat16)
+    q, ws = torch.zeros(64, dtype=torch.int8), torch.zeros(64, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="X must be float32"):
+        B.sp24_quantize(h, f[:1], q)
+    with pytest.raises(ValueError, match="s_x must be float32"):
+        B.sp24_quantize(f, h[:1], q)
+    with pytest.raises(ValueError, match="X must be float32"):
+        B.sp24_act_scale(h, 0.9999, f[:4], ws)
