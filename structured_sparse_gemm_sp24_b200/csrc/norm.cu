@@ -572,7 +572,7 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_fp8_kernel(const Quant
 // added in order through shared memory and the block writes one row of the
 // workspace; dgamma_kernel adds those rows in order (no atomics: the same
 // inputs give the same bits).  Groups keep the workspace short (509 x 768: 5.1
-// us with eight rows a block, 9.9 us with one).
+// us with four rows a block, 9.3 with one; 2000 x 768 with five 8.3 and 10.5).
 struct BackArgs {
   const void* dy;
   const void* dh;       // optional

@@ -6,8 +6,9 @@ import torch
 from oracle import sp24_oracle as O
 from structured_sparse_gemm_sp24_b200 import pipeline as P
 from structured_sparse_gemm_sp24_b200 import sp24 as B
-from tests.test_gpu_fp8 import (BF, F32, assert_product, exps, f64, product_case,  # noqa: F401
-                                rand, _device)
+from tests.test_gpu_fp8 import (BF, EPS, F32, HALF_BF16, NORM_REL, _device,  # noqa: F401
+                                assert_back, assert_codes_near, assert_product, back_inputs, exps,
+                                f64, product_case, rand, stored_sum)
 
 pytestmark = pytest.mark.gpu
 
@@ -197,3 +198,48 @@ def test_a_forced_split_keeps_one_cta_an_sm(monkeypatch):
         out = P.gemm_fp8(xq, e_x, vals, meta, e_w, 128 * 40)
         assert B.sp24_device_status() == B.SP24_OK
         assert_product(out, y, a, 1312, True)
+
+
+# -------------------------------- several rows a warp, and a group, one by one
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("res", [False, True])
+@pytest.mark.parametrize("k", [128, 256, 512])
+def test_norm_of_more_short_rows_than_warps(k, res, dt):
+    """Rows of one warp each, so many that every warp takes several (the next one
+    loaded ahead while this one's h is stored over x or over r)."""
+    m = 20003
+    x = rand((m, k), dt, k)
+    r = rand((m, k), dt, k + 1) if res else None
+    gamma = (1 + 0.2 * torch.randn(k, generator=torch.Generator().manual_seed(k))).to(dt)
+    h = stored_sum(x, r)
+    y, s = O.rmsnorm(f64(h), f64(gamma), EPS)
+    for target in (("x", "r", None) if res else (None,)):
+        a, b = x.cuda(), None if r is None else r.cuda()
+        o = P.rmsnorm_quant(a, gamma.cuda(), b, EPS, want_rstd=True,
+                            out_sum={"x": a, "r": b, None: None}[target])
+        assert torch.equal(o.h.cpu(), h)
+        np.testing.assert_allclose(f64(o.rstd), s, rtol=NORM_REL)
+        assert_codes_near(o.y, o.e_y, y, NORM_REL, k)
+    rc = None if r is None else r.cuda()
+    o = P.rmsnorm_quant(x.cuda(), gamma.cuda(), rc, EPS, B.SP24_BF16)
+    assert (np.abs(f64(o.y) - y) <= (HALF_BF16 + 2 * NORM_REL) * np.abs(y)).all()
+    s_x = torch.tensor([0.037], device="cuda")
+    o = P.rmsnorm_quant(x.cuda(), gamma.cuda(), rc, EPS, B.SP24_INT8, s_x=s_x)
+    v = y / float(s_x.double().cpu())
+    rel = NORM_REL + 2.0 ** -24
+    lo, hi = np.rint(np.clip(v * (1 - rel), -127, 127)), np.rint(np.clip(v * (1 + rel), -127, 127))
+    got = o.y.cpu().numpy().astype(np.float64)
+    assert ((got == lo) | (got == hi)).all()
+    assert B.sp24_device_status() == B.SP24_OK
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("m,k", [(8192, 768), (8191, 272), (5001, 1040), (3000, 2048), (3000, 4096)])
+def test_norm_backward_of_several_rows_a_group(m, k, dt):
+    """Groups of threads that take several rows each, an uneven number among them."""
+    h, gamma, dy, dh, rstd = back_inputs(m, k, dt, m + k)
+    for d in (None, dh):
+        dx, dg = P.rmsnorm_backward(dy.cuda(), h.cuda(), gamma.cuda(), rstd.cuda(),
+                                    dH=None if d is None else d.cuda())
+        assert_back(dx, dg, h, gamma, dy, d, rstd, dt is BF)
+    assert B.sp24_device_status() == B.SP24_OK
