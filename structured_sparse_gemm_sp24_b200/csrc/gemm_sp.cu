@@ -124,7 +124,11 @@ int pair_tokens(int impl) {
 // cannot overlap with the next tile.  Used only to rank the variants.  e4m3:
 // 0.59, 0.535 and 0.515 us a k-block of 256-, 240- and 224-token tiles (8192 x
 // 11008 x 4096: 194, 180 us; 8192 x 4096 x 4096: 73, 68, 66 us; the first has
-// room for three ring stages only).
+// room for three ring stages only).  A k-block's time follows the bytes that it
+// brings into an SM (16 KB of weights, 4 of metadata, 128 a token) and not the
+// tensor pipe alone: 8192 x 11008 x 4096 on 240 tokens takes 809 clocks a k-block
+// under the power cap, 727 with the token loads only, 661 with the weights' only
+// and 580 on resident operands, where the pipe needs 480.
 double est_time(int impl, int64_t m, int64_t n, int kblocks, int sms, int pairs, bool fp8) {
   const auto waves = [](int64_t tiles, int64_t units) {
     return static_cast<double>((tiles + units - 1) / units);
@@ -253,7 +257,10 @@ sp24_status make_plan(int64_t m, int64_t n, int kblocks, int dtype, Plan* p) {
   // kernel-family tests expect)
   const int64_t tiles128 = row_tiles * ((m + 127) / 128);
   // e4m3 has no single-SM kernel: what a pair tile cannot fill goes to split-K,
-  // unless its tiles are more than a launch's y and z number (16 bits each)
+  // unless its tiles are more than a launch's y and z number (16 bits each).  For
+  // 129 to 255 tokens that is not the best choice where the 128-token tiles pass
+  // one wave (160 x 11008 x 4096: 16.8 us, 224-token pairs 12.8; 160 x 22016 x 4096
+  // 29.7 and 20.3); at 128 tokens it is (11008: 11.5 and 12.5, 22016: 18.6 and 20.1).
   const bool fp8_split =
       fp8 && forced < 0 && (m < 256 || n < 256) && row_tiles <= 65535 && m <= 65535 * 128;
   const bool enough = m >= 128 || (fp8 && row_tiles > 65535);
@@ -309,7 +316,12 @@ sp24_status make_plan(int64_t m, int64_t n, int kblocks, int dtype, Plan* p) {
   // 5, 6 and 7 run correctly (SP24_SPLITK) but measured no better: at 3 CTAs
   // per SM a GPC holds fewer 5-CTA clusters than the 86 tiles need
   // (cudaOccupancyMaxActiveClusters: 82), and the second wave costs more
-  // than the shorter K loop saves.
+  // than the shorter K loop saves.  With the lean loop the model no longer holds
+  // where a split shares SMs: 11008 x 4096, weights from HBM, split 1 and 4, bf16
+  // M = 1 11.2 and 10.8 us, 16 11.2 and 11.3, 64 12.5 and 14.3, int8 8.1 and 8.6, 8.3
+  // and 8.9, 10.5 and 11.7.  It still picks the best split where CTAs do not share
+  // (4096 x 4096, split 4: bf16 M = 16 6.7 us, 1 9.5, 8 7.1; int8 5.1, 6.6, 5.5), and
+  // another split would change the bf16 sums' order.
   int split = 1;
   int64_t best = -1;
   const int cap = small_ring_ctas_per_sm(dtype, bn);

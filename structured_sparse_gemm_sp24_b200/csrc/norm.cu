@@ -482,8 +482,10 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_kernel(const NormArgs a) {
 constexpr int kQuantUnroll = 4;
 constexpr int kQuantThreads = 256;
 
-// Quotient by a fixed divisor of numbers below 2^31: with l = ceil(log2 d) and
-// mul = floor(2^32 (2^l - d) / d) + 1 it is (mulhi(n, mul) + n) >> l.
+// Quotient by a fixed divisor of numbers below 2^31 (the round-up method of
+// Granlund and Montgomery, "Division by invariant integers using multiplication",
+// 1994): with l = ceil(log2 d) and mul = floor(2^32 (2^l - d) / d) + 1 it is
+// (mulhi(n, mul) + n) >> l.
 struct FastDiv {
   uint32_t mul, shift;
   FastDiv(uint32_t d = 1) {
@@ -937,9 +939,12 @@ static sp24_status launch_norm(const NormArgs& a, cudaStream_t s) {
   if (c <= 1024 && (c <= 128 || sizeof(T) == 4 || a.m <= 2 * sm_count()))
     return launch_norm_t<T, OUT, 1, false, 1024, 1>(a, round32(c), s);
   // Long float32 rows without a residual, more than one an SM: three vectors a
-  // thread, whose registers hold the next row as well (777 x 11008: 12.8 us, two
-  // vectors without the next row 14.0; 2000 x 11008: 28.6 and 32.2).  With a
-  // residual, or a row an SM, two vectors (100 x 11008: 3.8 us, three 5.1).
+  // thread in two blocks an SM, whose 64 registers hold the next row as well but
+  // for a few values (8 bytes of spills for e4m3, 36 for the other outputs).
+  // Against two vectors without the next row: 777 x 11008 to e4m3 13.9 and 17.1 us,
+  // to int8 17.1 and 19.7, to bf16 12.8 and 15.4; 1000 x 9216 15.0 and 17.9; 2000 x
+  // 11008 29.2 and 39.3.  With a residual, or a row an SM, two vectors (100 x 11008:
+  // 3.9 us, three 5.1).
   if constexpr (sizeof(T) == 4) {
     if (c > 1024 && c <= 1536 && a.r == nullptr && a.m > sm_count())
       return launch_norm_t<T, OUT, 3, false, 512, 2, false>(a, round32((c + 2) / 3), s);
