@@ -202,10 +202,10 @@ def _ptr(t: Optional[torch.Tensor]):
     return t.data_ptr()
 
 
-def _f32(t: torch.Tensor, name: str) -> None:
+def _f32(t: Optional[torch.Tensor], name: str) -> None:
     """Refuses a tensor that the library would read as float32 and that is not (a
     shorter type would be read past its end)."""
-    if t.dtype != torch.float32:
+    if t is not None and t.dtype != torch.float32:
         raise ValueError(f"sp24: {name} must be float32, not {t.dtype}")
 
 

@@ -243,3 +243,14 @@ def test_norm_backward_of_several_rows_a_group(m, k, dt):
                                     dH=None if d is None else d.cuda())
         assert_back(dx, dg, h, gamma, dy, d, rstd, dt is BF)
     assert B.sp24_device_status() == B.SP24_OK
+
+
+def test_quantize_without_a_scale_is_an_argument_error():
+    x = torch.zeros((4, 256), device="cuda")
+    with pytest.raises(B.Sp24Error) as e:
+        P.quantize(x, None)
+    assert e.value.status == B.SP24_ERR_ARG
+    with pytest.raises(ValueError, match="float32"):
+        P.quantize(x.to(BF), torch.ones(1, device="cuda"))
+    with pytest.raises(ValueError, match="float32"):
+        P.act_scale(x.to(BF))
