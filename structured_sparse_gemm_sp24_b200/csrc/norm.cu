@@ -250,13 +250,14 @@ __device__ __forceinline__ Vec8<T> norm_sum(const Vec8<T>& x, const Vec8<T>& r, 
 // only the error of s can still move a code (8192 x 4096: 1 to 23 of 33.5 million
 // codes differ from those of 64 bits, 20 to 27 with y rounded to nearest, 19 to
 // 38 in plain fp32).
-// `last` is the bit to set in both halves.  s is irrational, so no product with
-// it is exact and the bit is set in all (a zero becomes the smallest subnormal),
-// unless s is a power of two: then only float32 products that fp32 does not
-// hold are inexact, those with a remainder (kAsk).  Rows of this kind are rare:
-// they are done again after the others, as the question in every row, or a loop
-// of its own there, costs registers (777 x 11008: 15.3 us a call; 14.0 this way
-// and 13.9 without).
+// `last` is the bit to set in both halves.  An s that is no power of two has no
+// finite binary fraction, so its products count as inexact and the bit is set in
+// all (a zero becomes the smallest subnormal; a product that is exact all the same,
+// 3 * 2/3, is moved by the error of s).  With a power of two only float32 products
+// that fp32 does not hold are inexact, those with a remainder (kAsk).  Rows of this
+// kind are rare: they are done again after the others, as the question in every
+// row, or a loop of its own there, costs registers (777 x 11008: 15.3 us a call;
+// 14.0 this way and 13.9 without).
 enum Rounding { kNearest, kOdd, kAsk };
 
 __device__ __forceinline__ bool norm_pow2(float2 s) {
