@@ -209,6 +209,17 @@ def _f32(t: Optional[torch.Tensor], name: str) -> None:
         raise ValueError(f"sp24: {name} must be float32, not {t.dtype}")
 
 
+def _operands(X: torch.Tensor, vals: torch.Tensor, dtype: int) -> None:
+    """Refuses product operands that are not bf16 or int8 as `dtype` says (one-byte
+    codes taken for bf16 would be read past their end).  Whole numbers of the same
+    size, the values' bits, pass."""
+    want = {SP24_BF16: torch.bfloat16, SP24_INT8: torch.int8}.get(dtype)
+    for t, name in ((X, "X"), (vals, "vals")):
+        if want is not None and t.dtype != want and (t.is_floating_point()
+                                                     or t.element_size() != want.itemsize):
+            raise ValueError(f"sp24: {name} must be {want} for this product, not {t.dtype}")
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:   # (current_stream() builds a Python object: 3 us a call)
         return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
@@ -336,6 +347,7 @@ def sp24_conv3x3(X: torch.Tensor, vals: torch.Tensor, meta: torch.Tensor, Cout: 
                  s_x: Optional[torch.Tensor], s_w: Optional[torch.Tensor], out_kind: int,
                  s_y: Optional[torch.Tensor], Y: torch.Tensor, stream=None) -> None:
     Bn, H, W, C = X.shape
+    _operands(X, vals, dtype)
     _check(lib().sp24_conv3x3(_ptr(X), Bn, H, W, C, _ptr(vals), _ptr(meta), Cout, dtype,
                               _ptr(s_x), _ptr(s_w), out_kind, _ptr(s_y), _ptr(Y),
                               _stream(stream)), "sp24_conv3x3")
@@ -345,6 +357,7 @@ def sp24_gemm(X: torch.Tensor, vals: torch.Tensor, meta: torch.Tensor, N: int, d
               s_x: Optional[torch.Tensor], s_w: Optional[torch.Tensor], out_kind: int,
               s_y: Optional[torch.Tensor], Y: torch.Tensor, stream=None) -> None:
     M, K = X.shape
+    _operands(X, vals, dtype)
     _check(lib().sp24_gemm(_ptr(X), M, K, _ptr(vals), _ptr(meta), N, dtype, _ptr(s_x),
                            _ptr(s_w), out_kind, _ptr(s_y), _ptr(Y), _stream(stream)),
            "sp24_gemm")

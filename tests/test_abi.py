@@ -261,3 +261,19 @@ def test_float32_inputs_are_checked(lib):
         B.sp24_quantize(f, h[:1], q)
     with pytest.raises(ValueError, match="X must be float32"):
         B.sp24_act_scale(h, 0.9999, f[:4], ws)
+
+
+def test_product_operands_are_checked(lib):
+    """e4m3 codes given to the bf16 product (or bf16 rows to the int8 one) are
+    refused before any CUDA call."""
+    import torch
+    bf, i8 = torch.zeros(4, 128, dtype=torch.bfloat16), torch.zeros(4, 128, dtype=torch.int8)
+    f8 = i8.view(torch.float8_e4m3fn)
+    y, meta = torch.zeros(4, 8, dtype=torch.bfloat16), torch.zeros(2048, dtype=torch.uint8)
+    for x, v, dt, name in ((f8, bf, B.SP24_BF16, "X"), (i8, bf, B.SP24_BF16, "X"),
+                           (bf, f8, B.SP24_BF16, "vals"), (bf, i8, B.SP24_INT8, "X"),
+                           (i8, f8, B.SP24_INT8, "vals")):
+        with pytest.raises(ValueError, match=f"{name} must be"):
+            B.sp24_gemm(x, v, meta, 8, dt, None, None, B.SP24_OUT_BF16, None, y)
+        with pytest.raises(ValueError, match=f"{name} must be"):
+            B.sp24_conv3x3(x.view(1, 2, 2, 128), v, meta, 8, dt, None, None, B.SP24_OUT_BF16, None, y)
